@@ -1,0 +1,499 @@
+"""Workloads of the routed layer's 4-bit experts and of its router in training.
+
+Four operators, each with its plain form in elementary torch operations:
+
+``forward_w4``         the layer forward with 4-bit expert weights and group scales
+``balance_loss``       per-expert counts and the load-balance loss of the router
+``route_backward``     gradient of the router logits (routing weights and balance loss)
+``finalize_backward``  gradients of the routing-weighted sum of expert outputs
+
+``own`` selects the framework's calls; otherwise the plain forms run.
+"""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+
+
+# ---------------------------------------------------------------- the cases
+
+def _w4(name, T, H, I, E, k, off, E_l, L, rg, rd, group, zeros, method=0, scaling=1.0):
+    return {"name": name, "op": "forward_w4", "T": T, "H": H, "I": I, "E": E, "k": k, "off": off,
+            "E_l": E_l, "L": L, "rg": rg, "rd": rd, "group": group, "zeros": zeros,
+            "method": method, "scaling": scaling}
+
+
+def listed():
+    return [
+        # one user's next token: 8 experts' weights and six dependent launches
+        _w4("w4 one token", 1, 2048, 768, 128, 8, 0, 128, 1, 16, 16, 128, False),
+        # a decode batch of many users with four adapters, the weight stream of nearly all experts
+        _w4("w4 decode 64", 64, 2048, 768, 128, 8, 0, 128, 4, 16, 16, 64, True),
+        # a prompt chunk between decode and prefill: tens of rows an expert
+        _w4("w4 chunk 384", 384, 2048, 768, 128, 8, 0, 128, 4, 16, 16, 128, False),
+        # a whole prompt: a hundred and more rows an expert, rank-64 adapters
+        _w4("w4 prefill 2048", 2048, 2048, 768, 128, 8, 0, 128, 4, 64, 64, 128, False),
+        # an expert-parallel shard of a layer with sizes that fill no tile, ranks not multiples of 8
+        _w4("w4 odd shard", 77, 1088, 416, 40, 6, 8, 24, 3, 20, 12, 32, True, 1, 2.5),
+        # a decode-sized batch: latency
+        {"name": "balance 64", "op": "balance_loss", "T": 64, "E": 128, "k": 8, "S": 1, "masked": 0.0},
+        # a training micro-batch of ragged, padded sequences
+        {"name": "balance 32768", "op": "balance_loss", "T": 32768, "E": 256, "k": 8, "S": 9, "masked": 0.1},
+        # the smallest router gradient, and a training micro-batch's
+        {"name": "router grad 64", "op": "route_backward", "T": 64, "E": 128, "k": 8, "S": 1,
+         "masked": 0.0, "method": 0, "balance": True},
+        {"name": "router grad 32768", "op": "route_backward", "T": 32768, "E": 256, "k": 8, "S": 9,
+         "masked": 0.1, "method": 1, "balance": True},
+        # a decode-sized batch, a training micro-batch, an expert-parallel shard with odd sizes
+        {"name": "finalize grad 16", "op": "finalize_backward", "T": 16, "H": 2048, "k": 8, "local": 1.0,
+         "scaling": 1.0},
+        {"name": "finalize grad 8192", "op": "finalize_backward", "T": 8192, "H": 2048, "k": 8, "local": 1.0,
+         "scaling": 1.0},
+        {"name": "finalize grad odd", "op": "finalize_backward", "T": 333, "H": 1088, "k": 5, "local": 0.4,
+         "scaling": 2.5},
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["forward_w4", "forward_w4", "balance_loss", "route_backward", "finalize_backward"])
+    if op == "forward_w4":
+        E = rng.randint(4, 128)
+        E_l = E if rng.random() < 0.5 else rng.randint(1, E)
+        c = _w4("", _log(rng, 1, 2048), 64 * rng.randint(2, 32), 32 * rng.randint(2, 24), E,
+                rng.randint(1, min(8, E)), rng.randint(0, E - E_l), E_l, rng.randint(0, 4),
+                rng.choice([0, 4, 8, 16, 20, 32, 64]), rng.choice([0, 4, 8, 12, 16, 32, 64]),
+                rng.choice([32, 64, 128]), rng.random() < 0.5, rng.randint(0, 1), rng.choice([1.0, 2.5]))
+        del c["name"]
+        return c
+    if op == "finalize_backward":
+        return {"op": op, "T": _log(rng, 1, 8192), "H": 64 * rng.randint(1, 32), "k": rng.randint(1, 8),
+                "local": rng.choice([1.0, 0.5, 0.1]), "scaling": rng.choice([1.0, 2.5])}
+    E = rng.randint(4, 256)
+    c = {"op": op, "T": _log(rng, 1, 32768), "E": E, "k": rng.randint(1, min(8, E)),
+         "S": _log(rng, 1, 32), "masked": rng.choice([0.0, 0.1, 0.6])}
+    if op == "route_backward":
+        c["method"] = rng.randint(0, 1)
+        c["balance"] = rng.random() < 0.75
+    return c
+
+
+# ---------------------------------------------------------------- the inputs
+
+def _gen(seed):
+    return torch.Generator(DEV).manual_seed(seed)
+
+
+def _quantised(g, E, K, N, group, zeros):
+    """Codes uint8 [E, K/2, N] (row 2i in the low nibble), scales bf16 and zero
+    points uint8 [E, ceil(K/group), N] of normal weights, as a quantiser leaves them."""
+    G = -(-K // group)
+    w = torch.zeros((E, G * group, N), device=DEV)
+    w[:, :K] = torch.randn((E, K, N), generator=g, device=DEV)
+    w = w.mul_(0.02).view(E, G, group, N)
+    if zeros:
+        lo, hi = w.amin(2).clamp(max=0.0), w.amax(2).clamp(min=0.0)
+        s = ((hi - lo) / 15).clamp(min=1e-8).to(torch.bfloat16)
+        z = (-lo / s.float()).round().clamp(0, 15)
+    else:
+        s = (w.abs().amax(2) / 7).clamp(min=1e-8).to(torch.bfloat16)
+        z = torch.full(s.shape, 8.0, device=DEV)
+    q = w.div_(s.float()[:, :, None]).add_(z[:, :, None]).round_().clamp_(0, 15)
+    q = q.view(E, G * group, N)[:, :K].to(torch.uint8)
+    codes = q[:, 0::2] | (q[:, 1::2] << 4)
+    return {"codes": codes.contiguous(), "scales": s, "zeros": z.to(torch.uint8) if zeros else None}
+
+
+def _bf16(g, sigma, *shape):
+    return (torch.randn(shape, generator=g, device=DEV) * sigma).to(torch.bfloat16)
+
+
+def _tokens(c, g):
+    """Mask and offsets of c["S"] ragged sequences (one in five empty), the rest of the batch unused."""
+    T, S = c["T"], c["S"]
+    mask = None
+    if c["masked"] > 0:
+        mask = (torch.rand(T, generator=g, device=DEV) >= c["masked"]).to(torch.uint8)
+    if S == 1:
+        return mask, None
+    length = torch.rand(S, generator=g, device=DEV) + 0.05
+    length = torch.where(torch.rand(S, generator=g, device=DEV) < 0.2, torch.zeros_like(length), length)
+    share = length.cumsum(0) / length.sum().clamp(min=1.0)
+    ends = (share * (T - T // 50)).floor().clamp(0, T).to(torch.int32)
+    return mask, torch.cat([torch.zeros(1, dtype=torch.int32, device=DEV), ends])
+
+
+def _routed(c, logits, method):
+    """Ids (ties to the lowest) and weights of the k largest logits."""
+    val, ids = torch.sort(logits, dim=1, descending=True, stable=True)
+    ids = ids[:, :c["k"]].to(torch.int32).contiguous()
+    ex = (val[:, :c["k"]] - val[:, :1]).exp()
+    den = (val - val[:, :1]).exp().sum(1, keepdim=True) if method else ex.sum(1, keepdim=True)
+    return ids, (ex / den).contiguous()
+
+
+def _shape(c):
+    from mixture_experts_layer_up_amd import binding
+    op = c["op"]
+    if op == "forward_w4":
+        return binding.Shape(c["T"], c["H"], c["I"], c["E"], c["k"], c["off"], c["E_l"], c["L"], c["rg"],
+                             c["rd"], c["scaling"], 0, c["method"])
+    if op == "finalize_backward":
+        return binding.Shape(c["T"], c["H"], 64, 64, c["k"], 0, 64, 0, 0, 0, c["scaling"], 0, 0)
+    return binding.Shape(c["T"], 64, 64, c["E"], c["k"], 0, c["E"], 0, 0, 0, 1.0, 0, c.get("method", 0))
+
+
+def prepare(case, seed):
+    c, g = case, _gen(seed)
+    T = c["T"]
+    s = {"case": c}
+    if c["op"] == "forward_w4":
+        H, I, E_l, L, rg, rd = c["H"], c["I"], c["E_l"], c["L"], c["rg"], c["rd"]
+        s["logits"] = torch.randn((T, c["E"]), generator=g, device=DEV)
+        s["hidden"] = _bf16(g, 1.0, T, H)
+        s["w13"] = _quantised(g, E_l, H, 2 * I, c["group"], c["zeros"])
+        s["w2"] = _quantised(g, E_l, I, H, c["group"], c["zeros"])
+        s["mapping"] = torch.randint(-1, max(L, 1), (T,), generator=g, device=DEV, dtype=torch.int32)
+        s["a_gu"], s["b_gu"] = _bf16(g, 0.02, L, E_l, rg, H), _bf16(g, 0.02, L, E_l, 2 * I, rg)
+        s["a_dn"], s["b_dn"] = _bf16(g, 0.02, L, E_l, rd, I), _bf16(g, 0.02, L, E_l, H, rd)
+        if own:  # laid out once, when a program loads its weights and adapters
+            from mixture_experts_layer_up_amd import binding
+            sh = s["shape"] = _shape(c)
+            fmt = s["format"] = binding.W4Format(c["group"], int(c["zeros"]))
+            s["packed"] = binding.pack_weights_w4(sh, fmt, s["w13"], s["w2"])
+            s["packed_a"] = binding.pack_lora_a(sh, s["a_gu"], s["a_dn"])
+            s["workspace"] = torch.empty(max(1, binding.workspace_size_w4(sh)), dtype=torch.uint8, device=DEV)
+        return s
+    if c["op"] == "finalize_backward":
+        n = T * c["k"]
+        local = torch.rand(n, generator=g, device=DEV) < c["local"]
+        order = torch.rand(n, generator=g, device=DEV).masked_fill(~local, 2.0).argsort()
+        perm = torch.empty(n, dtype=torch.int32, device=DEV)
+        perm[order] = torch.arange(n, dtype=torch.int32, device=DEV)
+        s["perm"] = perm.masked_fill(~local, -1)
+        s["d_out"], s["y"] = _bf16(g, 0.01, T, c["H"]), _bf16(g, 1.0, n, c["H"])
+        s["weights"] = torch.rand((T, c["k"]), generator=g, device=DEV).softmax(1)
+        s["d_y"] = torch.zeros((n, c["H"]), dtype=torch.bfloat16, device=DEV)
+    else:
+        s["logits"] = torch.randn((T, c["E"]), generator=g, device=DEV) + \
+            torch.randn(c["E"], generator=g, device=DEV)
+        s["mask"], s["offsets"] = _tokens(c, g)
+        s["ids"], s["weights"] = _routed(c, s["logits"], c.get("method", 0))
+        if c["op"] == "route_backward":
+            s["d_weights"] = torch.randn((T, c["k"]), generator=g, device=DEV) * 0.1
+            s["d_loss"] = torch.full((1,), 0.01, device=DEV)
+            if c["balance"]:  # a program holds these from its forward pass
+                seq, n = _sequences(T, c["S"], s["mask"], s["offsets"])
+                s["counts"] = _counts(s["ids"], seq, c["S"], c["E"])
+                s["tokens"] = n
+    if own:
+        s["shape"] = _shape(c)
+    return s
+
+
+# ---------------------------------------------------------------- the plain forms
+
+def _sequences(T, S, mask, offsets):
+    """Sequence of each token, S where it is in none or masked; tokens of each sequence (int32)."""
+    dev = DEV
+    if offsets is None:
+        seq = torch.zeros(T, dtype=torch.int64, device=dev)
+    else:
+        at = torch.arange(T, dtype=torch.int32, device=dev)
+        seq = torch.searchsorted(offsets[1:].contiguous(), at, right=True)
+    if mask is not None:
+        seq = torch.where(mask != 0, seq, torch.full_like(seq, S))
+    n = torch.zeros(S + 1, dtype=torch.int32, device=dev)
+    n.scatter_add_(0, seq, torch.ones(T, dtype=torch.int32, device=dev))
+    return seq, n[:S].contiguous()
+
+
+def _counts(ids, seq, S, E):
+    n = torch.zeros((S + 1) * E, dtype=torch.int32, device=DEV)
+    n.scatter_add_(0, (seq[:, None] * E + ids).view(-1),
+                   torch.ones(ids.numel(), dtype=torch.int32, device=DEV))
+    return n.view(S + 1, E)[:S].contiguous()
+
+
+def _softmax(x):
+    e = (x - x.amax(1, keepdim=True)).exp()
+    return e / e.sum(1, keepdim=True)
+
+
+def _plain_balance(s):
+    c = s["case"]
+    T, E, k, S = c["T"], c["E"], c["k"], c["S"]
+    seq, n = _sequences(T, S, s["mask"], s["offsets"])
+    counts = _counts(s["ids"], seq, S, E)
+    p = _softmax(s["logits"])
+    member = (seq == torch.arange(S, device=DEV)[:, None]).float()
+    per = n.clamp(min=1).float()[:, None]
+    mean = member @ p / per
+    loss = (counts.float() / per * mean).sum(1) * (E / k)
+    live = (n > 0).sum().clamp(min=1)
+    return {"loss": (loss.sum() / live).view(1), "counts": counts, "probs": mean, "tokens": n}
+
+
+def _plain_route_backward(s):
+    c = s["case"]
+    T, E, k, S = c["T"], c["E"], c["k"], c["S"]
+    seq, _ = _sequences(T, S, s["mask"], s["offsets"])
+    ids, w, dw = s["ids"].long(), s["weights"], s["d_weights"]
+    dot = (w * dw).sum(1, keepdim=True)
+    p = _softmax(s["logits"])
+    if c["method"] == 0:
+        d = torch.zeros((T, E), device=DEV).scatter_add_(1, ids, w * (dw - dot))
+    else:
+        d = (-p * dot).scatter_add_(1, ids, w * dw)
+    if c["balance"]:
+        per = s["tokens"].clamp(min=1).float()[:, None]
+        live = (s["tokens"] > 0).sum().clamp(min=1)
+        g = s["counts"].float() * (s["d_loss"] * E / k) / (per * per * live)
+        g = torch.cat([g, torch.zeros((1, E), device=DEV)])[seq]
+        d = d + p * (g - (p * g).sum(1, keepdim=True))
+    return torch.where((seq < S)[:, None], d, torch.zeros_like(d))
+
+
+def _plain_finalize_backward(s):
+    c = s["case"]
+    T, k, scale = c["T"], c["k"], c["scaling"]
+    perm = s["perm"].long()
+    local = (perm >= 0)[:, None]
+    d = s["d_out"].float()[:, None].expand(T, k, c["H"])
+    y = torch.where(local, s["y"][perm.clamp(min=0)].float(), torch.zeros((), device=DEV)).view(T, k, c["H"])
+    d_w = (d * y).sum(2) * scale
+    rows = (d * s["weights"][:, :, None] * scale).reshape(T * k, c["H"]).to(torch.bfloat16)
+    out = torch.zeros((T * k + 1, c["H"]), dtype=torch.bfloat16, device=DEV)
+    out[torch.where(perm >= 0, perm, torch.full_like(perm, T * k))] = rows
+    return {"d_expert_out": out[:T * k], "d_weights": d_w}
+
+
+def _touched(key):
+    """The keys that occur (one at least), ascending, and each key's place among them (-1 stays)."""
+    some = key[key >= 0].unique()
+    some = some if some.numel() else key.new_zeros(1)
+    return some, torch.where(key >= 0, torch.searchsorted(some, key), key)
+
+
+def _dequantised(q, which, K, group):
+    codes, scales = q["codes"][which], q["scales"][which].float()
+    E, _, N = codes.shape
+    w = torch.stack([codes & 15, codes >> 4], 2).view(E, K, N).float()
+    z = q["zeros"][which].float() if q["zeros"] is not None else torch.full(scales.shape, 8.0, device=DEV)
+    at = torch.arange(K, device=DEV) // group
+    return (w - z[:, at]) * scales[:, at]
+
+
+def _lora(x, pair, which, a, b):
+    """x A^T B^T with the stacks [.., r, K] and [.., N, r] of each row's (adapter, expert) pair."""
+    a = a.flatten(0, 1)[which].float().transpose(1, 2).contiguous()
+    b = b.flatten(0, 1)[which].float().transpose(1, 2).contiguous()
+    return _grouped(_grouped(x, pair, a), pair, b)
+
+
+def _grouped(x, key, w):
+    """x[i] @ w[key[i]], zero rows where key[i] is negative: one padded batched product."""
+    G, K, N = w.shape
+    n = x.shape[0]
+    key = torch.where(key >= 0, key, torch.full_like(key, G))
+    count = torch.zeros(G + 1, dtype=torch.int64, device=DEV)
+    count.scatter_add_(0, key, torch.ones_like(key))
+    order = key.argsort(stable=True)
+    first = count.cumsum(0) - count
+    rank = torch.empty_like(key)
+    rank[order] = torch.arange(n, device=DEV) - first[key[order]]
+    most = max(1, int(count[:G].max()))
+    at = torch.where(key < G, key * most + rank, torch.full_like(key, G * most))
+    padded = torch.zeros((G * most + 1, K), device=DEV)
+    padded[at] = x
+    y = torch.zeros((G * most + 1, N), device=DEV)
+    y[:G * most] = torch.bmm(padded[:G * most].view(G, most, K), w).view(G * most, N)
+    return torch.where((key < G)[:, None], y[at], torch.zeros((), device=DEV))
+
+
+def _plain_w4(s):
+    c = s["case"]
+    T, H, I, k, E_l, L = c["T"], c["H"], c["I"], c["k"], c["E_l"], c["L"]
+    ids, weights = _routed(c, s["logits"], c["method"])
+    e = ids.long().view(-1) - c["off"]
+    e = torch.where((e >= 0) & (e < E_l), e, torch.full_like(e, -1))
+    experts, key = _touched(e)
+    lora = s["mapping"].long()[:, None].expand(T, k).reshape(-1)
+    pairs, pair = _touched(torch.where((e >= 0) & (lora >= 0), lora * E_l + e, torch.full_like(e, -1)))
+    x = s["hidden"].float()[:, None].expand(T, k, H).reshape(T * k, H)
+    h = _grouped(x, key, _dequantised(s["w13"], experts, H, c["group"]))
+    if L > 0 and c["rg"] > 0:
+        h = h + _lora(x, pair, pairs, s["a_gu"], s["b_gu"])
+    gate, up = h[:, :I], h[:, I:]
+    act = gate / (1 + (-gate).exp()) * up
+    y = _grouped(act, key, _dequantised(s["w2"], experts, I, c["group"]))
+    if L > 0 and c["rd"] > 0:
+        y = y + _lora(act, pair, pairs, s["a_dn"], s["b_dn"])
+    out = (y.view(T, k, H) * weights[:, :, None]).sum(1) * c["scaling"]
+    return out.to(torch.bfloat16)
+
+
+# ---------------------------------------------------------------- one pass
+
+def _own_run(s):
+    from mixture_experts_layer_up_amd import binding
+    c, sh = s["case"], s["shape"]
+    if c["op"] == "forward_w4":
+        return binding.forward_w4(
+            sh, s["format"], s["hidden"], *s["packed"],
+            lora_a_gate_up=s["packed_a"][0], lora_b_gate_up=s["b_gu"],
+            lora_a_down=s["packed_a"][1], lora_b_down=s["b_dn"],
+            token_lora_mapping=s["mapping"], router_logits=s["logits"], workspace=s["workspace"])
+    if c["op"] == "finalize_backward":
+        d_y, d_w = binding.finalize_backward(sh, s["d_out"], s["y"],
+                                             {"expanded_idx_to_permuted_idx": s["perm"],
+                                              "topk_weights": s["weights"]}, d_expert_out=s["d_y"])
+        return {"d_expert_out": d_y, "d_weights": d_w}
+    if c["op"] == "balance_loss":
+        return binding.balance_loss(sh, s["logits"], s["ids"], token_mask=s["mask"],
+                                    seq_offsets=s["offsets"])
+    kept = {"counts": s["counts"], "tokens": s["tokens"]} if c["balance"] else None
+    return binding.route_backward(sh, s["logits"], s["ids"], s["weights"], d_topk_weights=s["d_weights"],
+                                  balance=kept, d_loss=s["d_loss"] if kept else None,
+                                  token_mask=s["mask"], seq_offsets=s["offsets"])
+
+
+def run(state):
+    if own:
+        return _own_run(state)
+    return {"forward_w4": _plain_w4, "balance_loss": _plain_balance, "route_backward": _plain_route_backward,
+            "finalize_backward": _plain_finalize_backward}[state["case"]["op"]](state)
+
+
+def work(case):
+    c = case
+    T, k = c["T"], c["k"]
+    if c["op"] == "forward_w4":
+        H, I, L = c["H"], c["I"], c["L"]
+        # uniform routing: each expert is one of a token's k with chance k / E
+        hit = 1 - (1 - k / c["E"]) ** T
+        slots = T * k * c["E_l"] / c["E"]
+        codes = 3 * H * I / 2 + 3 * H * I / c["group"] * (3 if c["zeros"] else 2)
+        pairs = L * c["E_l"] * (1 - (1 - k / c["E"] / (L + 1)) ** T)
+        lora = (2 * I * c["rg"] + H * c["rg"] + H * c["rd"] + I * c["rd"]) if L else 0
+        with_lora = slots * L / (L + 1)
+        return {"bytes": c["E_l"] * hit * codes + pairs * lora * 2 + T * H * 4 + T * c["E"] * 4 + T * 4,
+                "flops": slots * 6 * H * I + with_lora * 2 * lora}
+    if c["op"] == "finalize_backward":
+        rows = T * k * c["local"]
+        return {"bytes": T * c["H"] * 2 + rows * c["H"] * 4 + T * k * 12, "flops": rows * c["H"] * 3}
+    E, S = c["E"], c["S"]
+    extra = (T if c["masked"] > 0 else 0) + (4 * S if S > 1 else 0)
+    if c["op"] == "balance_loss":
+        return {"bytes": T * E * 4 + T * k * 4 + S * E * 8 + extra, "flops": T * E * 5}
+    return {"bytes": T * E * 8 + T * k * 12 + (S * E * 4 if c["balance"] else 0) + extra, "flops": T * E * 9}
+
+
+# ---------------------------------------------------------------- the definition in 64 bits
+
+def _owner(s):
+    """The sequence of each token as a host list entry, None where the token takes part in nothing."""
+    c = s["case"]
+    off = [0, c["T"]] if s["offsets"] is None else s["offsets"].tolist()
+    seq = [None] * c["T"]
+    for i in range(c["S"]):
+        for t in range(off[i], off[i + 1]):
+            seq[t] = i
+    if s["mask"] is not None:
+        seq = [i if m else None for i, m in zip(seq, s["mask"].tolist())]
+    return seq
+
+
+def _exact_router(s, c):
+    E, k, S = c["E"], c["k"], c["S"]
+    seq = _owner(s)
+    p = torch.softmax(s["logits"].double().cpu(), 1)
+    ids = s["ids"].long().cpu()
+    rows = [[t for t, i in enumerate(seq) if i == q] for q in range(S)]
+    live = max(1, sum(bool(r) for r in rows))
+    counts = torch.zeros((S, E), dtype=torch.float64)
+    mean = torch.zeros((S, E), dtype=torch.float64)
+    for q, r in enumerate(rows):
+        if r:
+            counts[q] = torch.bincount(ids[r].reshape(-1), minlength=E).double()
+            mean[q] = p[r].mean(0)
+    if c["op"] == "balance_loss":
+        loss = 0.0
+        for q, r in enumerate(rows):
+            if r:
+                loss += E * float((counts[q] / (k * len(r)) * mean[q]).sum()) / live
+        return {"loss": torch.tensor([loss], dtype=torch.float64), "counts": None, "probs": mean, "tokens": None}
+    w, dw = s["weights"].double().cpu(), s["d_weights"].double().cpu()
+    d = torch.zeros((c["T"], E), dtype=torch.float64)
+    inside = (w * dw).sum(1)
+    for j in range(k):
+        part = w[:, j] * (dw[:, j] - (inside if c["method"] == 0 else 0))
+        d[torch.arange(c["T"]), ids[:, j]] += part
+    if c["method"] == 1:
+        d -= p * inside[:, None]
+    for q, r in enumerate(rows):
+        if r and c["balance"]:
+            g = counts[q] * float(s["d_loss"]) * E / (k * len(r) ** 2 * live)
+            d[r] += p[r] * (g - (p[r] @ g)[:, None])
+    d[[t for t, i in enumerate(seq) if i is None]] = 0
+    return d
+
+
+def _exact_w4(s, c):
+    T, k, H, I, off, L = c["T"], c["k"], c["H"], c["I"], c["off"], c["L"]
+    logits = s["logits"].double()
+    ids = torch.sort(logits, dim=1, descending=True, stable=True).indices[:, :k]
+    full = torch.softmax(logits, 1)
+    w = full.gather(1, ids)
+    if c["method"] == 0:
+        w = w / w.sum(1, keepdim=True)
+    x, out = s["hidden"].double(), torch.zeros((T, H), dtype=torch.float64, device=DEV)
+
+    def weights(q, e, K):
+        code = q["codes"][e]
+        v = torch.empty((K, code.shape[1]), dtype=torch.float64, device=DEV)
+        v[0::2], v[1::2] = (code % 16).double(), torch.div(code, 16, rounding_mode="floor").double()
+        for b in range(-(-K // c["group"])):
+            part = slice(b * c["group"], (b + 1) * c["group"])
+            v[part] = (v[part] - (q["zeros"][e, b].double() if q["zeros"] is not None else 8)) * \
+                q["scales"][e, b].double()
+        return v
+
+    for e in range(c["E_l"]):
+        t, j = (ids == e + off).nonzero(as_tuple=True)
+        if not len(t):
+            continue
+        h = x[t] @ weights(s["w13"], e, H)
+        for n in range(L if c["rg"] else 0):
+            r = (s["mapping"][t] == n).nonzero()[:, 0]
+            h[r] += x[t[r]] @ s["a_gu"][n, e].double().T @ s["b_gu"][n, e].double().T
+        act = h[:, :I] * torch.sigmoid(h[:, :I]) * h[:, I:]
+        y = act @ weights(s["w2"], e, I)
+        for n in range(L if c["rd"] else 0):
+            r = (s["mapping"][t] == n).nonzero()[:, 0]
+            y[r] += act[r] @ s["a_dn"][n, e].double().T @ s["b_dn"][n, e].double().T
+        out[t] += y * w[t, j][:, None]  # a token has an expert once
+    return out * c["scaling"]
+
+
+def exact(case, seed):
+    c, s = case, prepare(case, seed)
+    if c["op"] == "forward_w4":
+        return _exact_w4(s, c)
+    if c["op"] == "finalize_backward":
+        d, y = s["d_out"].double(), s["y"].double()
+        d_y = torch.zeros_like(y)
+        d_w = torch.zeros((c["T"], c["k"]), dtype=torch.float64, device=DEV)
+        for j in range(c["k"]):
+            p = s["perm"].view(c["T"], c["k"])[:, j].long()
+            t = (p >= 0).nonzero()[:, 0]
+            d_y[p[t]] = d[t] * s["weights"][t, j].double()[:, None] * c["scaling"]
+            d_w[t, j] = (d[t] * y[p[t]]).sum(1) * c["scaling"]
+        return {"d_expert_out": d_y, "d_weights": d_w}
+    return _exact_router(s, c)
