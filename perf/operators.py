@@ -168,7 +168,7 @@ def prepare(case, seed):
             fmt = s["format"] = binding.W4Format(c["group"], int(c["zeros"]))
             s["packed"] = binding.pack_weights_w4(sh, fmt, s["w13"], s["w2"])
             s["packed_a"] = binding.pack_lora_a(sh, s["a_gu"], s["a_dn"])
-            s["workspace"] = torch.empty(max(1, binding.workspace_size_w4(sh)), dtype=torch.uint8, device=DEV)
+            s["workspace"] = torch.empty(max(1, binding.workspace_size_w4(sh, fmt)), dtype=torch.uint8, device=DEV)
         return s
     if c["op"] == "finalize_backward":
         n = T * c["k"]
