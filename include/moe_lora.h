@@ -370,6 +370,156 @@ int moe_lora_finalize(const moe_lora_shape *shape, const void *expert_out,
                       const int32_t *expanded_idx_to_permuted_idx, const float *topk_weights,
                       void *out, void *stream);
 
+/*
+ * 4-bit expert weights.  A weight of a projection is
+ *   w[k][n] = scales[k / group][n] * (codes[k][n] - zeros[k / group][n])
+ * with codes and zero points in 0..15 and bf16 scales, over groups of `group`
+ * consecutive K rows (the last group may be shorter).  Plain layout, per
+ * projection [E_l, K, N] (w13: K = H, N = 2I; w2: K = I, N = H):
+ *   codes   uint8 [E_l, K / 2, N]: row 2i in the low nibble, row 2i + 1 in
+ *           the high nibble
+ *   scales  bf16 [E_l, ceil(K / group), N]
+ *   zeros   uint8 [E_l, ceil(K / group), N] when the format has zero points,
+ *           else NULL and 8 everywhere (of a zero point the low 4 bits count)
+ */
+typedef struct moe_lora_w4_format {
+    int32_t group;        /* 32, 64 or 128 K rows per scale */
+    int32_t zero_points;  /* 0: none (8 everywhere), 1: one per group and column */
+} moe_lora_w4_format;
+
+typedef struct moe_lora_w4_weights {
+    void *codes;
+    void *scales;
+    void *zeros;
+} moe_lora_w4_weights;
+
+/*
+ * Quantises bf16 expert weights w13 [E_l, H, 2I], w2 [E_l, I, H] to that
+ * format, at load: per group and column the scale is the bf16 rounding of
+ * max|w| / 7, and codes are round(w / scale) + 8; with zero points the scale is
+ * that of (max(w, 0) - min(w, 0)) / 15, the zero point round(-min / scale) and
+ * codes round(w / scale) + zero point; all clamped to 0..15, ties to even.
+ * A group of zeros has scale 0.  Weights must be finite.
+ */
+int moe_lora_quantize_w4(const moe_lora_shape *shape, const moe_lora_w4_format *format, const void *w13,
+                         const void *w2, const moe_lora_w4_weights *q13, const moe_lora_w4_weights *q2,
+                         void *stream);
+
+/*
+ * One-time relayout of 4-bit expert weights into the order the products
+ * stream, as moe_lora_pack_weights does for bf16 (moe_lora_packed_w4_bytes
+ * bytes each, which = 0 w13, 1 w2; outputs 16-byte aligned, not overlapping
+ * the inputs).
+ */
+size_t moe_lora_packed_w4_bytes(const moe_lora_shape *shape, const moe_lora_w4_format *format, int which);
+
+int moe_lora_pack_weights_w4(const moe_lora_shape *shape, const moe_lora_w4_format *format,
+                             const moe_lora_w4_weights *q13, const moe_lora_w4_weights *q2,
+                             void *w13_packed, void *w2_packed, void *stream);
+
+/*
+ * The layer forward with 4-bit expert weights: moe_lora_forward with
+ * inputs->w13_packed / w2_packed written by moe_lora_pack_weights_w4 for
+ * `format`, and a workspace of moe_lora_workspace_size_w4 bytes.  Everything
+ * else (routing, bf16 LoRA stacks, expert parallelism, the side stream, events,
+ * expert_out, the empty batch) is as there.  The weights enter the products
+ * exactly; sums are fp32.  Rounded to bf16 are the LoRA shrink outputs, the
+ * activations and the output.  Without expert_out the slots' expert outputs
+ * stay fp32 until the routing-weighted sum, so `out` and a moe_lora_finalize of
+ * the (bf16) expert_out agree to the rounding of expert_out, not bitwise.  A
+ * token whose hidden row holds an infinity or NaN gets non-finite outputs.
+ */
+size_t moe_lora_workspace_size_w4(const moe_lora_shape *shape, const moe_lora_w4_format *format);
+
+int moe_lora_forward_w4(const moe_lora_shape *shape, const moe_lora_w4_format *format,
+                        const moe_lora_inputs *inputs, const moe_lora_routing *routing, void *out,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The router in training.  `tokens` says which tokens take part: NULL for all
+ * tokens as one sequence, else
+ *   token_mask    NULL, or uint8 [T]: a token with 0 is padding
+ *   seq_offsets   NULL (one sequence of all tokens; num_sequences = 1), or
+ *                 device int32 [S + 1], ascending: sequence s is tokens
+ *                 [seq_offsets[s], seq_offsets[s + 1]), may be empty; tokens
+ *                 outside [seq_offsets[0], seq_offsets[S]) are padding.
+ *                 Offsets are clamped to [0, T]; descending ones give
+ *                 unspecified values but no access outside the arrays.
+ *   num_sequences S, 1 .. 65535
+ * Logits, ids, weights and gradients of padding tokens are never used, so they
+ * may hold anything.
+ */
+typedef struct moe_lora_tokens {
+    const uint8_t *token_mask;
+    const int32_t *seq_offsets;
+    int32_t num_sequences;
+} moe_lora_tokens;
+
+/*
+ * Balance loss of the router with per-expert counts (device arrays,
+ * caller-owned).  With p = softmax(router_logits) over all E experts, and N_s
+ * tokens of sequence s that take part:
+ *   expert_counts [S, E] int32  slots of those tokens with that id
+ *   expert_probs  [S, E] fp32   mean of p over those tokens (0 when N_s = 0)
+ *   seq_tokens    [S] int32     N_s
+ *   loss          fp32 [1]      mean over the sequences with N_s > 0 of
+ *                 E / (k N_s) * sum_e expert_counts * expert_probs; 0 when no
+ *                 token takes part.  Perfect balance gives 1.
+ * Counts are of global expert ids; ids outside [0, E) are not counted.  A row
+ * of logits that is -inf everywhere has p = 0.
+ */
+typedef struct moe_lora_balance {
+    float *loss;
+    int32_t *expert_counts;
+    float *expert_probs;
+    int32_t *seq_tokens;
+} moe_lora_balance;
+
+/* Uses num_tokens, num_experts and top_k of `shape`.  `workspace`: at least
+ * moe_lora_balance_workspace_size(shape, S) bytes, 256-byte aligned, any
+ * contents; NULL when that is 0 (small batches; also for an invalid shape). */
+size_t moe_lora_balance_workspace_size(const moe_lora_shape *shape, int32_t num_sequences);
+
+int moe_lora_balance_loss(const moe_lora_shape *shape, const float *router_logits,
+                          const int32_t *topk_ids, const moe_lora_tokens *tokens,
+                          const moe_lora_balance *balance, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/*
+ * Gradient of the router logits, d_logits fp32 [T, E], written completely
+ * (rows of padding tokens are 0).  The sum of
+ *   - the routing weights' part when d_topk_weights (fp32 [T, k]) is given: the
+ *     gradient through topk_weights as moe_lora_route computes them
+ *     (routing_method of `shape`; the choice of experts is constant).  Needs
+ *     topk_ids and topk_weights; slots with an id outside [0, E) add nothing.
+ *   - the balance loss's part when `balance` and d_loss (device fp32 [1], the
+ *     gradient of the loss) are given: expert_counts and seq_tokens as
+ *     moe_lora_balance_loss wrote them for the same `tokens` (loss and
+ *     expert_probs are not read and may be NULL).  Counts are constants.
+ * At least one part is given.  router_logits may be NULL when only the
+ * routing weights' part of routing_method 0 is asked for.
+ */
+int moe_lora_route_backward(const moe_lora_shape *shape, const float *router_logits,
+                            const int32_t *topk_ids, const float *topk_weights,
+                            const float *d_topk_weights, const moe_lora_tokens *tokens,
+                            const moe_lora_balance *balance, const float *d_loss, float *d_logits,
+                            void *stream);
+
+/*
+ * Gradients of moe_lora_finalize for d_out bf16 [T, H]:
+ *   d_expert_out   bf16 [T*k, H] or NULL: row p of local slot x = t * k + j is
+ *                  routed_scaling_factor * topk_weights[x] * d_out[t]; rows of
+ *                  no slot (for routed batches [P, T*k)) are not written
+ *   d_topk_weights fp32 [T, k] or NULL: routed_scaling_factor *
+ *                  <d_out[t], expert_out[p]>, 0 for slots that are not local
+ * One at least is given; d_expert_out needs topk_weights, d_topk_weights needs
+ * expert_out.  bf16 pointers are 16-byte aligned.  A permuted index outside
+ * [-1, T*k) counts as -1.
+ */
+int moe_lora_finalize_backward(const moe_lora_shape *shape, const void *d_out, const void *expert_out,
+                               const int32_t *expanded_idx_to_permuted_idx, const float *topk_weights,
+                               void *d_expert_out, float *d_topk_weights, void *stream);
+
 /* Static description of a status code. */
 const char *moe_lora_strerror(int status);
 

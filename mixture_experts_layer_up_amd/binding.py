@@ -40,6 +40,25 @@ class Shape(ctypes.Structure):
     ]
 
 
+class W4Format(ctypes.Structure):
+    """4-bit expert weights: K rows per scale (32, 64 or 128), zero points (0 or 1)."""
+    _fields_ = [("group", ctypes.c_int32), ("zero_points", ctypes.c_int32)]
+
+
+class W4Weights(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("codes", "scales", "zeros")]
+
+
+class Tokens(ctypes.Structure):
+    _fields_ = [("token_mask", ctypes.c_void_p), ("seq_offsets", ctypes.c_void_p),
+                ("num_sequences", ctypes.c_int32)]
+
+
+class Balance(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in (
+        "loss", "expert_counts", "expert_probs", "seq_tokens")]
+
+
 class Routing(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in (
         "topk_ids", "topk_weights", "expert_counts", "expert_offsets",
@@ -103,6 +122,28 @@ def load_library(path: str = LIB_PATH):
     lib.moe_lora_forward_no_alloc.restype = ctypes.c_int
     lib.moe_lora_finalize.argtypes = [P(Shape), vp, vp, vp, vp, vp]
     lib.moe_lora_finalize.restype = ctypes.c_int
+    W4 = P(W4Format)
+    lib.moe_lora_workspace_size_w4.argtypes = [P(Shape), W4]
+    lib.moe_lora_workspace_size_w4.restype = ctypes.c_size_t
+    lib.moe_lora_packed_w4_bytes.argtypes = [P(Shape), W4, ctypes.c_int]
+    lib.moe_lora_packed_w4_bytes.restype = ctypes.c_size_t
+    lib.moe_lora_quantize_w4.argtypes = [P(Shape), W4, vp, vp, P(W4Weights), P(W4Weights), vp]
+    lib.moe_lora_quantize_w4.restype = ctypes.c_int
+    lib.moe_lora_pack_weights_w4.argtypes = [P(Shape), W4, P(W4Weights), P(W4Weights), vp, vp, vp]
+    lib.moe_lora_pack_weights_w4.restype = ctypes.c_int
+    lib.moe_lora_forward_w4.argtypes = [P(Shape), W4, P(Inputs), P(Routing), vp, vp,
+                                        ctypes.c_size_t, vp]
+    lib.moe_lora_forward_w4.restype = ctypes.c_int
+    lib.moe_lora_balance_workspace_size.argtypes = [P(Shape), ctypes.c_int32]
+    lib.moe_lora_balance_workspace_size.restype = ctypes.c_size_t
+    lib.moe_lora_balance_loss.argtypes = [P(Shape), vp, vp, P(Tokens), P(Balance), vp,
+                                          ctypes.c_size_t, vp]
+    lib.moe_lora_balance_loss.restype = ctypes.c_int
+    lib.moe_lora_route_backward.argtypes = [P(Shape), vp, vp, vp, vp, P(Tokens), P(Balance), vp,
+                                            vp, vp]
+    lib.moe_lora_route_backward.restype = ctypes.c_int
+    lib.moe_lora_finalize_backward.argtypes = [P(Shape), vp, vp, vp, vp, vp, vp, vp]
+    lib.moe_lora_finalize_backward.restype = ctypes.c_int
     lib.moe_lora_strerror.argtypes = [ctypes.c_int]
     lib.moe_lora_strerror.restype = ctypes.c_char_p
     _lib = lib
@@ -258,8 +299,9 @@ def route(shape: Shape, router_logits: Optional[torch.Tensor] = None,
 def _inputs(shape: Shape, hidden, w13_packed, w2_packed, lora_a_gate_up, lora_b_gate_up,
             lora_a_down, lora_b_down, token_lora_mapping, router_logits, topk_ids, topk_weights,
             routing_bias, stage_events, expert_out, side_stream, fork_event, join_event,
-            input_flags):
-    """The moe_lora_inputs struct of one forward call (keeps its event array alive)."""
+            input_flags, w4: Optional[W4Format] = None):
+    """The moe_lora_inputs struct of one forward call (keeps its event array alive).
+    ``w4``: the expert weights are packed 4-bit ones of that format."""
     T, H, I, E, k = shape.num_tokens, shape.hidden, shape.inter, shape.num_experts, shape.top_k
     E_l, L, rg, rd = shape.local_num_experts, shape.num_loras, shape.rank_gate_up, shape.rank_down
     outer = 1 if shape.lora_shared_outer else E_l
@@ -276,8 +318,10 @@ def _inputs(shape: Shape, hidden, w13_packed, w2_packed, lora_a_gate_up, lora_b_
         _ptr(routing_bias, torch.float32, (E,), "routing_bias"),
         _ptr(topk_ids, torch.int32, (T, k), "topk_ids"),
         _ptr(topk_weights, torch.float32, (T, k), "topk_weights"),
-        _ptr(w13_packed, _BF16, (E_l, H, 2 * I), "w13_packed"),
-        _ptr(w2_packed, _BF16, (E_l, I, H), "w2_packed"),
+        *(_ptr(w, _BF16, plain, name) if w4 is None else
+          _ptr(w, torch.uint8, (packed_w4_bytes(shape, w4, which),), name)
+          for which, (w, plain, name) in enumerate((
+              (w13_packed, (E_l, H, 2 * I), "w13_packed"), (w2_packed, (E_l, I, H), "w2_packed")))),
         _ptr(lora_a_gate_up, _BF16, packed_lora_a_shape(shape, 0), "lora_a_gate_up (packed)")
         if gu else None,
         _ptr(lora_b_gate_up, _BF16, (L, E_l, 2 * I, rg), "lora_b_gate_up") if gu else None,
@@ -367,6 +411,238 @@ def finalize(shape: Shape, expert_out: torch.Tensor, routing: Dict[str, torch.Te
         _ptr(w, torch.float32, (T, k), "topk_weights"),
         _ptr(out, _BF16, (T, H), "out"), _stream()))
     return out
+
+
+class _on:
+    """The device that holds every given tensor, made current; its current stream."""
+
+    def __init__(self, *tensors):
+        devices = {t.device for t in tensors if t is not None}
+        if len(devices) != 1 or next(iter(devices)).type != "cuda":
+            raise MoELoRAError(f"tensors must be on one GPU, got {sorted(map(str, devices))}")
+        self.device = devices.pop()
+        self.stream = torch.cuda.current_stream(self.device).cuda_stream
+        self.guard = None
+
+    def __enter__(self):
+        if self.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def workspace_size_w4(shape: Shape, fmt: W4Format) -> int:
+    return int(load_library().moe_lora_workspace_size_w4(ctypes.byref(shape), ctypes.byref(fmt)))
+
+
+def packed_w4_bytes(shape: Shape, fmt: W4Format, which: int) -> int:
+    """Bytes of a packed 4-bit weight (which: 0 w13, 1 w2)."""
+    return int(load_library().moe_lora_packed_w4_bytes(ctypes.byref(shape), ctypes.byref(fmt), which))
+
+
+def w4_shapes(shape: Shape, fmt: W4Format, which: int):
+    """Plain shapes (codes, scales and zero points) of a 4-bit weight."""
+    E_l, H, I = shape.local_num_experts, shape.hidden, shape.inter
+    K, N = (H, 2 * I) if which == 0 else (I, H)
+    return (E_l, K // 2, N), (E_l, -(-K // fmt.group), N)
+
+
+def _w4_struct(shape: Shape, fmt: W4Format, which: int, q: Dict) -> W4Weights:
+    codes, groups = w4_shapes(shape, fmt, which)
+    name = ("w13", "w2")[which]
+    if fmt.zero_points and q.get("zeros") is None:
+        raise MoELoRAError(f"{name} zeros are missing (the format has zero points)")
+    return W4Weights(_ptr(q["codes"], torch.uint8, codes, name + " codes"),
+                     _ptr(q["scales"], _BF16, groups, name + " scales"),
+                     _ptr(q["zeros"], torch.uint8, groups, name + " zeros")
+                     if fmt.zero_points else None)
+
+
+def quantize_w4(shape: Shape, fmt: W4Format, w13: torch.Tensor, w2: torch.Tensor):
+    """4-bit weights of w13 [E_l, H, 2I] and w2 [E_l, I, H] (bf16): two dicts of
+    ``codes``, ``scales`` and ``zeros`` (None without zero points)."""
+    E_l, H, I = shape.local_num_experts, shape.hidden, shape.inter
+    with _on(w13, w2) as stream:
+        out = []
+        for which in (0, 1):
+            codes, groups = w4_shapes(shape, fmt, which)
+            new = lambda s, dt: torch.empty(s, dtype=dt, device=w13.device)  # noqa: E731
+            out.append({"codes": new(codes, torch.uint8), "scales": new(groups, torch.bfloat16),
+                        "zeros": new(groups, torch.uint8) if fmt.zero_points else None})
+        _check(load_library().moe_lora_quantize_w4(
+            ctypes.byref(shape), ctypes.byref(fmt), _ptr(w13, _BF16, (E_l, H, 2 * I), "w13"),
+            _ptr(w2, _BF16, (E_l, I, H), "w2"), ctypes.byref(_w4_struct(shape, fmt, 0, out[0])),
+            ctypes.byref(_w4_struct(shape, fmt, 1, out[1])), stream))
+    return out[0], out[1]
+
+
+def pack_weights_w4(shape: Shape, fmt: W4Format, w13: Dict, w2: Dict):
+    """Packed copies (uint8, one dimension) of two 4-bit weights given as dicts
+    of ``codes``, ``scales`` and ``zeros`` (:func:`quantize_w4`)."""
+    lib = load_library()
+    every = [q.get(n) for q in (w13, w2) for n in ("codes", "scales", "zeros")]
+    with _on(*every) as stream:
+        s13, s2 = _w4_struct(shape, fmt, 0, w13), _w4_struct(shape, fmt, 1, w2)
+        p13, p2 = (torch.empty(packed_w4_bytes(shape, fmt, which), dtype=torch.uint8,
+                               device=w13["codes"].device) for which in (0, 1))
+        _check(lib.moe_lora_pack_weights_w4(
+            ctypes.byref(shape), ctypes.byref(fmt), ctypes.byref(s13), ctypes.byref(s2),
+            p13.data_ptr(), p2.data_ptr(), stream))
+    return p13, p2
+
+
+def forward_w4(shape: Shape, fmt: W4Format, hidden: torch.Tensor, w13_packed: torch.Tensor,
+               w2_packed: torch.Tensor, lora_a_gate_up=None, lora_b_gate_up=None,
+               lora_a_down=None, lora_b_down=None, token_lora_mapping=None,
+               router_logits=None, topk_ids=None, topk_weights=None, routing_bias=None,
+               out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+               routing: Optional[Dict[str, torch.Tensor]] = None,
+               stage_events: Optional[Sequence[int]] = None,
+               expert_out: Optional[torch.Tensor] = None,
+               side_stream: Optional[int] = None, fork_event: Optional[int] = None,
+               join_event: Optional[int] = None,
+               input_flags: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """:func:`forward` with 4-bit expert weights, packed by :func:`pack_weights_w4`
+    for ``fmt``; the other arguments are those of :func:`forward`."""
+    T, H = shape.num_tokens, shape.hidden
+    with _on(hidden, w13_packed, w2_packed, lora_a_gate_up, lora_b_gate_up, lora_a_down, lora_b_down,
+             token_lora_mapping, router_logits, topk_ids, topk_weights, routing_bias, out, workspace,
+             expert_out, input_flags, *(routing.values() if routing is not None else ())) as stream:
+        if out is None and expert_out is None:
+            out = torch.empty((T, H), dtype=torch.bfloat16, device=hidden.device)
+        inputs, _ev = _inputs(shape, hidden, w13_packed, w2_packed, lora_a_gate_up, lora_b_gate_up,
+                              lora_a_down, lora_b_down, token_lora_mapping, router_logits, topk_ids,
+                              topk_weights, routing_bias, stage_events, expert_out, side_stream,
+                              fork_event, join_event, input_flags, w4=fmt)
+        rs = _routing_struct(routing) if routing is not None else None
+        if workspace is None:
+            workspace = torch.empty(max(workspace_size_w4(shape, fmt), 1), dtype=torch.uint8,
+                                    device=hidden.device)
+        _check(load_library().moe_lora_forward_w4(
+            ctypes.byref(shape), ctypes.byref(fmt), ctypes.byref(inputs),
+            ctypes.byref(rs) if rs is not None else None, _ptr(out, _BF16, (T, H), "out"),
+            _ptr(workspace, None, None, "workspace"),
+            workspace.numel() * workspace.element_size(), stream))
+    return out
+
+
+def _tokens(shape: Shape, token_mask, seq_offsets):
+    """(moe_lora_tokens pointer or None, number of sequences)."""
+    if token_mask is None and seq_offsets is None:
+        return None, 1
+    S = 1
+    if seq_offsets is not None:
+        if seq_offsets.dim() != 1 or seq_offsets.numel() < 2:
+            raise MoELoRAError("seq_offsets needs one entry more than there are sequences")
+        S = seq_offsets.numel() - 1
+    return ctypes.byref(Tokens(
+        _ptr(token_mask, (torch.uint8, torch.bool), (shape.num_tokens,), "token_mask"),
+        _ptr(seq_offsets, torch.int32, (S + 1,), "seq_offsets"), S)), S
+
+
+def balance_loss(shape: Shape, router_logits: torch.Tensor, topk_ids: torch.Tensor,
+                 token_mask: Optional[torch.Tensor] = None,
+                 seq_offsets: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None) -> Dict[str, torch.Tensor]:
+    """The router's balance loss over the tokens that take part: ``loss`` fp32 [1],
+    ``counts`` int32 [S, E], ``probs`` fp32 [S, E], ``tokens`` int32 [S].
+
+    ``token_mask`` (uint8 or bool [T]): 0 is padding.  ``seq_offsets`` (int32
+    [S + 1]): sequences of the batch; None is one sequence of all tokens.
+    :func:`route_backward` takes the result for the loss's gradient."""
+    T, E, k = shape.num_tokens, shape.num_experts, shape.top_k
+    lib = load_library()
+    with _on(router_logits, topk_ids, token_mask, seq_offsets, workspace) as stream:
+        tokens, S = _tokens(shape, token_mask, seq_offsets)
+        dev = router_logits.device
+        need = int(lib.moe_lora_balance_workspace_size(ctypes.byref(shape), S))
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        r = {"loss": torch.empty(1, dtype=torch.float32, device=dev),
+             "counts": torch.empty((S, E), dtype=torch.int32, device=dev),
+             "probs": torch.empty((S, E), dtype=torch.float32, device=dev),
+             "tokens": torch.empty(S, dtype=torch.int32, device=dev)}
+        _check(lib.moe_lora_balance_loss(
+            ctypes.byref(shape), _ptr(router_logits, torch.float32, (T, E), "router_logits"),
+            _ptr(topk_ids, torch.int32, (T, k), "topk_ids"), tokens,
+            ctypes.byref(Balance(r["loss"].data_ptr(), r["counts"].data_ptr(),
+                                 r["probs"].data_ptr(), r["tokens"].data_ptr())),
+            _ptr(workspace, None, None, "workspace"),
+            workspace.numel() * workspace.element_size() if workspace is not None else 0, stream))
+    return r
+
+
+def route_backward(shape: Shape, router_logits: Optional[torch.Tensor],
+                   topk_ids: Optional[torch.Tensor] = None,
+                   topk_weights: Optional[torch.Tensor] = None,
+                   d_topk_weights: Optional[torch.Tensor] = None,
+                   balance: Optional[Dict[str, torch.Tensor]] = None,
+                   d_loss: Optional[torch.Tensor] = None,
+                   token_mask: Optional[torch.Tensor] = None,
+                   seq_offsets: Optional[torch.Tensor] = None,
+                   d_logits: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of the router logits, fp32 [T, E]: the part of the routing weights
+    (``d_topk_weights`` fp32 [T, k]) plus that of the balance loss (``balance`` as
+    :func:`balance_loss` returned it for the same tokens, ``d_loss`` fp32 [1]).
+    Rows of tokens that take no part are 0."""
+    T, E, k = shape.num_tokens, shape.num_experts, shape.top_k
+    if (balance is None) != (d_loss is None):
+        raise MoELoRAError("balance and d_loss are given together")
+    kept = (balance["counts"], balance["tokens"]) if balance is not None else ()
+    with _on(router_logits, topk_ids, topk_weights, d_topk_weights, d_loss, token_mask, seq_offsets,
+             d_logits, *kept) as stream:
+        tokens, S = _tokens(shape, token_mask, seq_offsets)
+        bal = None
+        if balance is not None:
+            bal = ctypes.byref(Balance(None, _ptr(kept[0], torch.int32, (S, E), "counts"), None,
+                                       _ptr(kept[1], torch.int32, (S,), "tokens")))
+        if d_logits is None:
+            some = next(t for t in (router_logits, d_topk_weights, topk_ids) if t is not None)
+            d_logits = torch.empty((T, E), dtype=torch.float32, device=some.device)
+        _check(load_library().moe_lora_route_backward(
+            ctypes.byref(shape), _ptr(router_logits, torch.float32, (T, E), "router_logits"),
+            _ptr(topk_ids, torch.int32, (T, k), "topk_ids"),
+            _ptr(topk_weights, torch.float32, (T, k), "topk_weights"),
+            _ptr(d_topk_weights, torch.float32, (T, k), "d_topk_weights"), tokens, bal,
+            _ptr(d_loss, torch.float32, (1,), "d_loss"),
+            _ptr(d_logits, torch.float32, (T, E), "d_logits"), stream))
+    return d_logits
+
+
+def finalize_backward(shape: Shape, d_out: torch.Tensor, expert_out: Optional[torch.Tensor],
+                      routing: Dict[str, torch.Tensor],
+                      topk_weights: Optional[torch.Tensor] = None,
+                      d_expert_out: Optional[torch.Tensor] = None,
+                      d_topk_weights: Optional[torch.Tensor] = None,
+                      expert_out_grad: bool = True, weights_grad: bool = True):
+    """Gradients of :func:`finalize` for ``d_out`` bf16 [T, H]: (``d_expert_out``
+    bf16 [T*k, H], ``d_topk_weights`` fp32 [T, k]), None for the one not asked for.
+    Rows of ``d_expert_out`` that belong to no slot are not written (undefined when
+    allocated here)."""
+    T, H, k = shape.num_tokens, shape.hidden, shape.top_k
+    perm = routing["expanded_idx_to_permuted_idx"]
+    w = topk_weights if topk_weights is not None else routing.get("topk_weights")
+    with _on(d_out, expert_out, perm, w, d_expert_out, d_topk_weights) as stream:
+        if expert_out_grad and d_expert_out is None:
+            d_expert_out = torch.empty((T * k, H), dtype=torch.bfloat16, device=d_out.device)
+        if weights_grad and d_topk_weights is None:
+            d_topk_weights = torch.empty((T, k), dtype=torch.float32, device=d_out.device)
+        if not expert_out_grad:
+            d_expert_out = None
+        if not weights_grad:
+            d_topk_weights = None
+        _check(load_library().moe_lora_finalize_backward(
+            ctypes.byref(shape), _ptr(d_out, _BF16, (T, H), "d_out"),
+            _ptr(expert_out, _BF16, (T * k, H), "expert_out"),
+            _ptr(perm, torch.int32, (T * k,), "expanded_idx_to_permuted_idx"),
+            _ptr(w, torch.float32, (T, k), "topk_weights"),
+            _ptr(d_expert_out, _BF16, (T * k, H), "d_expert_out"),
+            _ptr(d_topk_weights, torch.float32, (T, k), "d_topk_weights"), stream))
+    return d_expert_out, d_topk_weights
 
 
 def layer_from_host(cfg, inputs: Dict, device="cuda"):

@@ -18,7 +18,10 @@
 #include <mutex>
 
 #include "kernels.h"
+#include "kernels_router.h"
+#include "kernels_w4.h"
 #include "moe_lora.h"
+#include "w4_layout.h"
 
 using namespace moe_lora;
 
@@ -65,6 +68,24 @@ int validate_shape(const moe_lora_shape *s)
 bool lora_gate_up_active(const moe_lora_shape *s) { return s->num_loras > 0 && s->rank_gate_up > 0; }
 bool lora_down_active(const moe_lora_shape *s) { return s->num_loras > 0 && s->rank_down > 0; }
 
+int validate_w4(const moe_lora_w4_format *f)
+{
+    if (!f)
+        return MOE_LORA_ERR_INVALID_ARG;
+    if (f->group != 32 && f->group != 64 && f->group != 128)
+        return MOE_LORA_ERR_UNSUPPORTED_SHAPE;
+    if (f->zero_points != 0 && f->zero_points != 1)
+        return MOE_LORA_ERR_INVALID_ARG;
+    return MOE_LORA_OK;
+}
+
+int validate_w4_weights(const moe_lora_w4_format *f, const moe_lora_w4_weights *q)
+{
+    if (!q->codes || !q->scales || (q->zeros != nullptr) != (f->zero_points != 0))
+        return MOE_LORA_ERR_INVALID_ARG;
+    return aligned(q->scales, 2) ? MOE_LORA_OK : MOE_LORA_ERR_MISALIGNED;
+}
+
 // Workspace regions; every offset is a multiple of 256 bytes.
 struct Layout {
     size_t ids, weights, counts, offsets, exp2perm, perm2exp, seg_offsets, seg_slots;
@@ -73,7 +94,8 @@ struct Layout {
     size_t total;
 };
 
-Layout make_layout(const moe_lora_shape *s)
+// w4: the format of a forward with 4-bit expert weights, else null
+Layout make_layout(const moe_lora_shape *s, const moe_lora_w4_format *w4 = nullptr)
 {
     const size_t n = (size_t)s->num_tokens * s->top_k;
     const size_t el = (size_t)s->local_num_experts;
@@ -94,9 +116,10 @@ Layout make_layout(const moe_lora_shape *s)
     L.seg_offsets = take((segs + 1) * 4);
     L.seg_slots = take(n * 4);
     L.perm_scratch = take(permute_scratch_bytes((int)n, (int)el, s->num_loras));
-    L.tile_rows = gemm_tile_rows((int)n, (int)el, s->hidden, s->inter,
-                                 lora_gate_up_active(s) ? s->rank_gate_up : 0,
-                                 lora_down_active(s) ? s->rank_down : 0);
+    L.tile_rows = w4 ? gemm_w4_tile_rows((int)n, (int)el)
+                     : gemm_tile_rows((int)n, (int)el, s->hidden, s->inter,
+                                      lora_gate_up_active(s) ? s->rank_gate_up : 0,
+                                      lora_down_active(s) ? s->rank_down : 0);
     L.max_tiles = max_gemm_tiles((int)n, (int)el, L.tile_rows);
     L.tiles = take((size_t)L.max_tiles * sizeof(int4));
     L.tile_count = take(sizeof(int32_t));
@@ -104,7 +127,8 @@ Layout make_layout(const moe_lora_shape *s)
     L.s_gu = take(lora_gate_up_active(s) ? n * round8(s->rank_gate_up) * 2 : 0);
     L.act = take(n * (size_t)s->inter * 2);
     L.s_dn = take(lora_down_active(s) ? n * round8(s->rank_down) * 2 : 0);
-    L.y = take(n * (size_t)s->hidden * 2);
+    // expert outputs: bf16, or with 4-bit weights fp32 (finalize_f32.hip)
+    L.y = take(n * (size_t)s->hidden * (w4 ? 4 : 2));
     L.total = o;
     return L;
 }
@@ -372,10 +396,51 @@ int validate_inputs(const moe_lora_shape *shape, const moe_lora_inputs *in,
     return MOE_LORA_OK;
 }
 
-// The layer forward on a workspace the caller or the library provides.
+// One of the two expert products with 4-bit weights, from the bf16 product's
+// argument block (same rows, work list and LoRA operands).
+int enqueue_gemm_w4(const GemmArgs &g, const moe_lora_w4_format *w4, bool gated, void *y, bool y_f32,
+                    hipStream_t st)
+{
+    const W4Layout l = w4_layout(g.E_l, g.K, g.n_canon, w4->group, w4->zero_points != 0);
+    const uint8_t *packed = reinterpret_cast<const uint8_t *>(g.Wp);
+    GemmW4Args a{};
+    a.X = g.X;
+    a.gather_by_token = g.gather_by_token;
+    a.K = g.K;
+    a.N = g.n_canon;
+    a.codes = packed;
+    a.scales = reinterpret_cast<const uint16_t *>(packed + l.scales);
+    a.zeros = w4->zero_points ? packed + l.zeros : nullptr;
+    a.k_units = l.k_units;
+    a.n_groups = l.n_groups;
+    a.group = w4->group;
+    a.n_slabs = l.n_slabs;
+    a.S = g.S;
+    a.LB = g.LB;
+    a.r = g.r;
+    a.rp = g.rp;
+    a.L = g.L;
+    a.n_canon = g.n_canon;
+    a.lb_shared = g.lb_shared;
+    a.mapping = g.mapping;
+    a.tiles = g.tiles;
+    a.tile_count = g.tile_count;
+    a.n_tiles = g.n_tiles;
+    a.tile_rows = g.tile_rows;
+    a.perm2exp = g.perm2exp;
+    a.E_l = g.E_l;
+    a.k = g.k;
+    a.I = g.I;
+    a.Y = y;
+    a.y_f32 = y_f32;
+    return check(launch_gemm_w4(a, gated, st));
+}
+
+// The layer forward on a workspace the caller or the library provides; w4 is
+// null for bf16 expert weights.
 int forward_impl(const moe_lora_shape *shape, const moe_lora_inputs *in,
                  const moe_lora_routing *routing, void *out, void *workspace,
-                 size_t workspace_bytes, void *stream)
+                 size_t workspace_bytes, void *stream, const moe_lora_w4_format *w4 = nullptr)
 {
     MOE_TRY(validate_shape(shape));
     if (!in)
@@ -396,7 +461,7 @@ int forward_impl(const moe_lora_shape *shape, const moe_lora_inputs *in,
     const bool from_logits = in->router_logits != nullptr;
     const bool gu = lora_gate_up_active(shape);
     const bool dn = lora_down_active(shape);
-    const Layout lay = make_layout(shape);
+    const Layout lay = make_layout(shape, w4);
     if (workspace_bytes < lay.total)
         return MOE_LORA_ERR_WORKSPACE_TOO_SMALL;
 
@@ -523,7 +588,7 @@ int forward_impl(const moe_lora_shape *shape, const moe_lora_inputs *in,
     };
     g1.n_slabs = slabs(g1.NT);
     g1.zeros = static_cast<const uint16_t *>(zeros);
-    MOE_TRY(check(launch_gemm_gate_up(g1, st)));
+    MOE_TRY(w4 ? enqueue_gemm_w4(g1, w4, true, act, false, st) : check(launch_gemm_gate_up(g1, st)));
     MOE_TRY(record(ev, 3, st));
 
     if (dn) {
@@ -559,10 +624,15 @@ int forward_impl(const moe_lora_shape *shape, const moe_lora_inputs *in,
     g2.n_slabs = slabs(g2.NT);
     g2.zeros = static_cast<const uint16_t *>(zeros);
     g2.lb_shared = shape->lora_shared_outer;
-    MOE_TRY(check(launch_gemm_down(g2, st)));
+    const bool y_f32 = w4 && !expert_out;
+    MOE_TRY(w4 ? enqueue_gemm_w4(g2, w4, false, y, y_f32, st) : check(launch_gemm_down(g2, st)));
     MOE_TRY(record(ev, 5, st));
 
-    if (!expert_out) {
+    if (y_f32) {
+        FinalizeF32Args fa{reinterpret_cast<const float *>(y), r.exp2perm, weights,
+                           static_cast<uint16_t *>(out), T, H, k, shape->routed_scaling_factor};
+        MOE_TRY(check(launch_finalize_f32(fa, st)));
+    } else if (!expert_out) {
         FinalizeArgs fa{y, r.exp2perm, weights, static_cast<uint16_t *>(out), T, H, k,
                         shape->routed_scaling_factor};
         MOE_TRY(check(launch_finalize(fa, st)));
@@ -640,6 +710,203 @@ int moe_lora_finalize(const moe_lora_shape *shape, const void *expert_out,
                     topk_weights, static_cast<uint16_t *>(out), shape->num_tokens,
                     shape->hidden, shape->top_k, shape->routed_scaling_factor};
     return check(launch_finalize(fa, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_lora_workspace_size_w4(const moe_lora_shape *shape, const moe_lora_w4_format *format)
+{
+    if (validate_shape(shape) != MOE_LORA_OK || validate_w4(format) != MOE_LORA_OK)
+        return 0;
+    return make_layout(shape, format).total;
+}
+
+size_t moe_lora_packed_w4_bytes(const moe_lora_shape *shape, const moe_lora_w4_format *format, int which)
+{
+    if (validate_shape(shape) != MOE_LORA_OK || validate_w4(format) != MOE_LORA_OK ||
+        (which != 0 && which != 1))
+        return 0;
+    const int H = shape->hidden, I = shape->inter;
+    return w4_layout(shape->local_num_experts, which == 0 ? H : I, which == 0 ? 2 * I : H, format->group,
+                     format->zero_points != 0).bytes;
+}
+
+int moe_lora_quantize_w4(const moe_lora_shape *shape, const moe_lora_w4_format *format, const void *w13,
+                         const void *w2, const moe_lora_w4_weights *q13, const moe_lora_w4_weights *q2,
+                         void *stream)
+{
+    MOE_TRY(validate_shape(shape));
+    MOE_TRY(validate_w4(format));
+    if (!w13 || !w2 || !q13 || !q2)
+        return MOE_LORA_ERR_INVALID_ARG;
+    MOE_TRY(validate_w4_weights(format, q13));
+    MOE_TRY(validate_w4_weights(format, q2));
+    if (!aligned(w13, 2) || !aligned(w2, 2))
+        return MOE_LORA_ERR_MISALIGNED;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const int E_l = shape->local_num_experts, H = shape->hidden, I = shape->inter;
+    auto args = [&](const void *w, const moe_lora_w4_weights *q, int K, int N) {
+        return QuantizeW4Args{static_cast<const uint16_t *>(w), static_cast<uint8_t *>(q->codes),
+                              static_cast<uint16_t *>(q->scales), static_cast<uint8_t *>(q->zeros),
+                              E_l, K, N, format->group};
+    };
+    MOE_TRY(check(launch_quantize_w4(args(w13, q13, H, 2 * I), st)));
+    return check(launch_quantize_w4(args(w2, q2, I, H), st));
+}
+
+int moe_lora_pack_weights_w4(const moe_lora_shape *shape, const moe_lora_w4_format *format,
+                             const moe_lora_w4_weights *q13, const moe_lora_w4_weights *q2,
+                             void *w13_packed, void *w2_packed, void *stream)
+{
+    MOE_TRY(validate_shape(shape));
+    MOE_TRY(validate_w4(format));
+    if (!q13 || !q2 || !w13_packed || !w2_packed)
+        return MOE_LORA_ERR_INVALID_ARG;
+    MOE_TRY(validate_w4_weights(format, q13));
+    MOE_TRY(validate_w4_weights(format, q2));
+    if (!aligned(w13_packed, 16) || !aligned(w2_packed, 16))
+        return MOE_LORA_ERR_MISALIGNED;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const int E_l = shape->local_num_experts, H = shape->hidden, I = shape->inter;
+    auto args = [&](const moe_lora_w4_weights *q, void *dst, int K, int N, int gate_cols) {
+        return PackW4Args{static_cast<const uint8_t *>(q->codes), static_cast<const uint16_t *>(q->scales),
+                          static_cast<const uint8_t *>(q->zeros), static_cast<uint8_t *>(dst),
+                          E_l, K, N, gate_cols, format->group};
+    };
+    MOE_TRY(check(launch_pack_w4(args(q13, w13_packed, H, 2 * I, I), st)));
+    return check(launch_pack_w4(args(q2, w2_packed, I, H, 0), st));
+}
+
+int moe_lora_forward_w4(const moe_lora_shape *shape, const moe_lora_w4_format *format,
+                        const moe_lora_inputs *inputs, const moe_lora_routing *routing, void *out,
+                        void *workspace, size_t workspace_bytes, void *stream)
+{
+    MOE_TRY(validate_shape(shape));
+    MOE_TRY(validate_w4(format));
+    return forward_impl(shape, inputs, routing, out, workspace, workspace_bytes, stream, format);
+}
+
+} // extern "C"
+
+namespace {
+
+int validate_tokens(const moe_lora_tokens *t)
+{
+    if (!t)
+        return MOE_LORA_OK;
+    if (t->num_sequences < 1 || t->num_sequences > 65535)
+        return MOE_LORA_ERR_UNSUPPORTED_SHAPE;
+    if (!t->seq_offsets && t->num_sequences != 1)
+        return MOE_LORA_ERR_INVALID_ARG;
+    return MOE_LORA_OK;
+}
+
+TokenSet token_set(const moe_lora_shape *shape, const moe_lora_tokens *t)
+{
+    if (!t)
+        return TokenSet{nullptr, nullptr, shape->num_tokens, 1};
+    return TokenSet{t->token_mask, t->seq_offsets, shape->num_tokens, t->num_sequences};
+}
+
+} // namespace
+
+extern "C" {
+
+size_t moe_lora_balance_workspace_size(const moe_lora_shape *shape, int32_t num_sequences)
+{
+    if (validate_shape(shape) != MOE_LORA_OK || num_sequences < 1 || num_sequences > 65535)
+        return 0;
+    return balance_workspace(shape->num_tokens, shape->num_experts, num_sequences);
+}
+
+int moe_lora_balance_loss(const moe_lora_shape *shape, const float *router_logits,
+                          const int32_t *topk_ids, const moe_lora_tokens *tokens,
+                          const moe_lora_balance *balance, void *workspace, size_t workspace_bytes,
+                          void *stream)
+{
+    MOE_TRY(validate_shape(shape));
+    MOE_TRY(validate_tokens(tokens));
+    if (!balance || !balance->loss || !balance->expert_counts || !balance->expert_probs ||
+        !balance->seq_tokens)
+        return MOE_LORA_ERR_INVALID_ARG;
+    if (shape->num_tokens > 0 && (!router_logits || !topk_ids))
+        return MOE_LORA_ERR_INVALID_ARG;
+    BalanceArgs a{};
+    a.tok = token_set(shape, tokens);
+    a.logits = router_logits;
+    a.ids = topk_ids;
+    a.E = shape->num_experts;
+    a.k = shape->top_k;
+    const size_t need = balance_workspace(a.tok.T, a.E, a.tok.S);
+    if (need > 0) {
+        if (!workspace)
+            return MOE_LORA_ERR_INVALID_ARG;
+        if (workspace_bytes < need)
+            return MOE_LORA_ERR_WORKSPACE_TOO_SMALL;
+        if (!aligned(workspace, kAlign))
+            return MOE_LORA_ERR_MISALIGNED;
+        balance_layout(&a, workspace);
+    }
+    a.loss = balance->loss;
+    a.counts = balance->expert_counts;
+    a.probs = balance->expert_probs;
+    a.tokens = balance->seq_tokens;
+    return check(launch_balance(a, static_cast<hipStream_t>(stream)));
+}
+
+int moe_lora_route_backward(const moe_lora_shape *shape, const float *router_logits,
+                            const int32_t *topk_ids, const float *topk_weights,
+                            const float *d_topk_weights, const moe_lora_tokens *tokens,
+                            const moe_lora_balance *balance, const float *d_loss, float *d_logits,
+                            void *stream)
+{
+    MOE_TRY(validate_shape(shape));
+    MOE_TRY(validate_tokens(tokens));
+    if ((balance != nullptr) != (d_loss != nullptr))
+        return MOE_LORA_ERR_INVALID_ARG;
+    if (balance && (!balance->expert_counts || !balance->seq_tokens))
+        return MOE_LORA_ERR_INVALID_ARG;
+    if (shape->num_tokens == 0)
+        return MOE_LORA_OK;
+    if (!d_logits || (!d_topk_weights && !balance))
+        return MOE_LORA_ERR_INVALID_ARG;
+    if (d_topk_weights && (!topk_ids || !topk_weights))
+        return MOE_LORA_ERR_INVALID_ARG;
+    if ((balance || shape->routing_method == 1) && !router_logits)
+        return MOE_LORA_ERR_INVALID_ARG;
+    RouteBackwardArgs a{};
+    a.tok = token_set(shape, tokens);
+    a.logits = router_logits;
+    a.ids = topk_ids;
+    a.weights = topk_weights;
+    a.d_weights = d_topk_weights;
+    a.counts = balance ? balance->expert_counts : nullptr;
+    a.tokens = balance ? balance->seq_tokens : nullptr;
+    a.d_loss = d_loss;
+    a.d_logits = d_logits;
+    a.E = shape->num_experts;
+    a.k = shape->top_k;
+    a.method = shape->routing_method;
+    return check(launch_route_backward(a, static_cast<hipStream_t>(stream)));
+}
+
+int moe_lora_finalize_backward(const moe_lora_shape *shape, const void *d_out, const void *expert_out,
+                               const int32_t *expanded_idx_to_permuted_idx, const float *topk_weights,
+                               void *d_expert_out, float *d_topk_weights, void *stream)
+{
+    MOE_TRY(validate_shape(shape));
+    if (shape->num_tokens == 0)
+        return MOE_LORA_OK;
+    if (!d_out || !expanded_idx_to_permuted_idx || (!d_expert_out && !d_topk_weights))
+        return MOE_LORA_ERR_INVALID_ARG;
+    if ((d_topk_weights && !expert_out) || (d_expert_out && !topk_weights))
+        return MOE_LORA_ERR_INVALID_ARG;
+    if (!aligned(d_out, 16) || !aligned(expert_out, 16) || !aligned(d_expert_out, 16))
+        return MOE_LORA_ERR_MISALIGNED;
+    FinalizeBackwardArgs a{static_cast<const uint16_t *>(d_out), static_cast<const uint16_t *>(expert_out),
+                           expanded_idx_to_permuted_idx, topk_weights,
+                           static_cast<uint16_t *>(d_expert_out), d_topk_weights,
+                           shape->num_tokens * shape->top_k, shape->hidden, shape->top_k,
+                           shape->routed_scaling_factor};
+    return check(launch_finalize_backward(a, static_cast<hipStream_t>(stream)));
 }
 
 const char *moe_lora_strerror(int status)
