@@ -399,7 +399,7 @@ int validate_inputs(const moe_lora_shape *shape, const moe_lora_inputs *in,
 // One of the two expert products with 4-bit weights, from the bf16 product's
 // argument block (same rows, work list and LoRA operands).
 int enqueue_gemm_w4(const GemmArgs &g, const moe_lora_w4_format *w4, bool gated, void *y, bool y_f32,
-                    hipStream_t st)
+                    int n_slots, hipStream_t st)
 {
     const W4Layout l = w4_layout(g.E_l, g.K, g.n_canon, w4->group, w4->zero_points != 0);
     const uint8_t *packed = reinterpret_cast<const uint8_t *>(g.Wp);
@@ -422,11 +422,14 @@ int enqueue_gemm_w4(const GemmArgs &g, const moe_lora_w4_format *w4, bool gated,
     a.L = g.L;
     a.n_canon = g.n_canon;
     a.lb_shared = g.lb_shared;
+    a.lb_stacks = g.L * (g.lb_shared ? 1 : g.E_l);
     a.mapping = g.mapping;
     a.tiles = g.tiles;
     a.tile_count = g.tile_count;
     a.n_tiles = g.n_tiles;
     a.tile_rows = g.tile_rows;
+    a.n_slots = n_slots;
+    a.n_busy = n_slots < g.E_l ? n_slots : g.E_l;
     a.perm2exp = g.perm2exp;
     a.E_l = g.E_l;
     a.k = g.k;
@@ -588,7 +591,7 @@ int forward_impl(const moe_lora_shape *shape, const moe_lora_inputs *in,
     };
     g1.n_slabs = slabs(g1.NT);
     g1.zeros = static_cast<const uint16_t *>(zeros);
-    MOE_TRY(w4 ? enqueue_gemm_w4(g1, w4, true, act, false, st) : check(launch_gemm_gate_up(g1, st)));
+    MOE_TRY(w4 ? enqueue_gemm_w4(g1, w4, true, act, false, T * k, st) : check(launch_gemm_gate_up(g1, st)));
     MOE_TRY(record(ev, 3, st));
 
     if (dn) {
@@ -625,7 +628,7 @@ int forward_impl(const moe_lora_shape *shape, const moe_lora_inputs *in,
     g2.zeros = static_cast<const uint16_t *>(zeros);
     g2.lb_shared = shape->lora_shared_outer;
     const bool y_f32 = w4 && !expert_out;
-    MOE_TRY(w4 ? enqueue_gemm_w4(g2, w4, false, y, y_f32, st) : check(launch_gemm_down(g2, st)));
+    MOE_TRY(w4 ? enqueue_gemm_w4(g2, w4, false, y, y_f32, T * k, st) : check(launch_gemm_down(g2, st)));
     MOE_TRY(record(ev, 5, st));
 
     if (y_f32) {

@@ -39,11 +39,12 @@ struct GemmW4Args {
     const uint16_t *S;        // shrink outputs [n, rp] by slot x, or null
     const uint16_t *LB;       // [L, E_l (shared: 1), n_canon, r] or null
     int r, rp, L, n_canon;    // n_canon: output columns of the unpacked weight
-    int lb_shared;
+    int lb_shared, lb_stacks; // one LB stack per adapter; stacks in LB
     const int32_t *mapping;   // [T] or null
     const int4 *tiles;        // work list written by the permute kernel
     const int32_t *tile_count;
     int n_tiles, tile_rows;   // list length (upper bound), rows per tile
+    int n_slots, n_busy;      // slots n, and experts they can touch: min(n, E_l)
     const int32_t *perm2exp;  // [n]
     int E_l, k, I;
     void *Y;                  // gate_up: bf16 act [n, I]; down: [n, n_canon]
@@ -62,6 +63,7 @@ struct FinalizeF32Args {
 // Rows per work-list tile for n slots over E_l local experts.
 int gemm_w4_tile_rows(int n_slots, int E_l);
 hipError_t launch_gemm_w4(const GemmW4Args &a, bool gated, hipStream_t s);
+hipError_t launch_gemm_w4_many(const GemmW4Args &a, bool gated, hipStream_t s);  // tiles of 32, 64 rows
 hipError_t launch_finalize_f32(const FinalizeF32Args &a, hipStream_t s);
 hipError_t launch_pack_w4(const PackW4Args &a, hipStream_t s);
 hipError_t launch_quantize_w4(const QuantizeW4Args &a, hipStream_t s);

@@ -72,7 +72,7 @@ __global__ __launch_bounds__(256) void pack_w4_scales_kernel(PackW4Args a)
         const size_t src = ((size_t)e * l.n_groups + g) * a.N + w4_column(slab, tile, c, a.I);
         reinterpret_cast<uint16_t *>(a.dst + l.scales)[f] = a.scales[src];
         if (a.zeros)
-            a.dst[l.zeros + f] = a.zeros[src] & 15;
+            a.dst[l.zeros + f] = 16 + (a.zeros[src] & 15);
     }
 }
 

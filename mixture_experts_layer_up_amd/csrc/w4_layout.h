@@ -14,12 +14,13 @@
 //           One 16-byte load per lane and half is 1 KiB contiguous.
 //   scales  bf16 at ((e * NS + s) * NG + g) * 64 + (column % 16) * 4 + tile:
 //           a lane's four tiles are one 8-byte load
-//   zeros   bytes in the same order (formats with zero points only)
-// Row counts that are not a multiple of 64 pad the last unit with code 0;
-// the kernels skip the padded 32-row chunk.
+//   zeros   bytes 16 + z in the same order (formats with zero points only):
+//           what the products subtract, one conversion from float
+// Row counts that are not whole steps of 128 rows (two units) are padded with
+// units of code 0, which meet zero activations.
 //
 // Nibble order inside a word.  The MFMA operand wants bf16 pairs (rows 2j,
-// 2j + 1) in one register.  With (16 + q) / 16 = bits 0x3f80 | q << 3, the
+// 2j + 1) in one register.  With 16 + q = bits 0x4180 | q << 3, the
 // code of row 2j sits at bit 3 + 4j and that of row 2j + 1 at bit 19 + 4j,
 // both modulo 32 (the last nibble wraps): rotating the word right by 4j and
 // one and-or then make the pair, 7 instructions for 8 weights.
@@ -41,7 +42,7 @@ constexpr int kW4UnitBytes = 2048;   // 64 x 64 codes
 
 struct W4Layout {
     int n_slabs;     // 64-column slabs: N / 64
-    int k_units;     // ceil(K / 64)
+    int k_units;     // units that cover K, in whole steps
     int n_groups;    // ceil(K / group)
     size_t scales;   // byte offset of the scales region
     size_t zeros;    // byte offset of the zero points (= bytes when there are none)
@@ -52,7 +53,7 @@ MOE_LORA_W4_HD inline W4Layout w4_layout(int E_l, int K, int N, int group, bool 
 {
     W4Layout l;
     l.n_slabs = N / 64;
-    l.k_units = (K + kW4UnitK - 1) / kW4UnitK;
+    l.k_units = (K + 2 * kW4UnitK - 1) / (2 * kW4UnitK) * 2;
     l.n_groups = (K + group - 1) / group;
     const size_t slabs = (size_t)E_l * l.n_slabs;
     l.scales = slabs * l.k_units * kW4UnitBytes;          // a multiple of 2048

@@ -69,11 +69,11 @@ def test_null_format_and_bad_shape(lib):
 
 @pytest.mark.parametrize("H,I,group,zeros", [(2048, 768, 128, 0), (64, 32, 32, 1), (1088, 416, 64, 1)])
 def test_packed_bytes(lib, H, I, group, zeros):
-    """Codes of whole 64-row units, a bf16 scale and a zero-point byte per group and column."""
+    """Codes in whole steps of 128 rows, a bf16 scale and a zero-point byte per group and column."""
     shape = _shape(hidden=H, inter=I)
     fmt = binding.W4Format(group, zeros)
     for which, (K, N) in enumerate(((H, 2 * I), (I, H))):
-        want = 128 * N * (-(-K // 64) * 32 + -(-K // group) * (2 + zeros))
+        want = 128 * N * (-(-K // 128) * 64 + -(-K // group) * (2 + zeros))
         assert binding.packed_w4_bytes(shape, fmt, which) == want
 
 
