@@ -16,22 +16,18 @@
 namespace moe_lora {
 namespace {
 
-#ifndef W4_D
-#define W4_D 2
-#endif
-#ifndef W4_PANEL
-#define W4_PANEL 8
-#endif
-#ifndef W4_W
-#define W4_W 3
-#endif
-constexpr int kRing = W4_D;              // steps in flight per wave
-constexpr int kPanelSteps = W4_PANEL;        // steps whose activations are staged at a time
+constexpr int kRing = 2;         // steps in flight per wave
+constexpr int kExpandSteps = 2;  // LoRA expand steps in flight
+
+// Steps whose activations are staged at a time.  Half of a 2048-row K leaves
+// LDS for three blocks per CU (64 tokens, 128 experts: 40 us for gate_up, 49 us
+// with all of it); blocks of 8 waves, few by definition, take it whole.
+constexpr int panel_steps(int NW) { return NW == 8 ? 16 : 8; }
 
 template <int NW, int G, bool kGated, bool kZeros>
-__global__ __launch_bounds__(NW * kWave, W4_W) void expert_gemm_w4_kernel(GemmW4Args a, int ks_log)
+__global__ __launch_bounds__(NW * kWave, 3) void expert_gemm_w4_kernel(GemmW4Args a, int ks_log)
 {
-    constexpr int D = kRing;
+    constexpr int D = kRing, kPanelSteps = panel_steps(NW);
     constexpr int kXs = 128 / G * 16;  // group sums of a step
     extern __shared__ u32x4 lds[];     // [S chunk][lane], [K chunk][lane], group sums; at the end the K shares
     const int lane = threadIdx.x & (kWave - 1);
@@ -74,9 +70,8 @@ __global__ __launch_bounds__(NW * kWave, W4_W) void expert_gemm_w4_kernel(GemmW4
         const int ps = min(kPanelSteps, n_steps - p0);
         const int sb = p0 + ((ks * ps) >> ks_log);  // this wave's steps
         const int ns = p0 + (((ks + 1) * ps) >> ks_log) - sb;
-        unsigned long long used = 0;
-        ExpandStep e{-1, 0};
-        u32x4 eb[kNS];
+        const bool expand = a.S && p0 == 0 && ks == 0 && active;
+        Expand<1, 1, kExpandSteps> ex;
         // the first codes are on their way before the rows are known
         StepW4<G> st[D];
 #pragma unroll
@@ -88,28 +83,25 @@ __global__ __launch_bounds__(NW * kWave, W4_W) void expert_gemm_w4_kernel(GemmW4
             arow += (lane >> 4) * 8;
             for (int c = wave; c < s_chunks; c += NW)
                 lds[c * kWave + lane] = load_s(a, slot, c, lane);
-            if (a.S && ks == 0 && active) {  // its first operands travel while the activations are staged
-                used = adapters_used(adapters, 1);
-                e = next_expand(e, &used, a.r);
-                if (e.l >= 0)
-                    load_expand(eb, a, w, e, I, lane);
-            }
+            if (expand)  // its first operands travel while the activations are staged
+                ex.start(adapters_used(adapters, 1), a, w, I, lane);
         } else {
             lds_barrier();  // the panel before is done with
         }
         for (int t = wave; t < ps; t += NW) {
             u32x4 v[kStepChunks];
             load_unit(v, arow, p0 + t, a.K);
-            store_unit<1, G>(v, frag + t * kStepChunks * kWave, xs + t * kXs, lane);
+            store_unit<1, G, kZeros>(v, p0 + t, a.K, frag + t * kStepChunks * kWave, xs + t * kXs, lane);
         }
         lds_barrier();
         if (!active)
             continue;
-        expand_all<1>(acc, eb, e, used, a, w, I, adapters, 1, lds, lane);
+        if (expand)
+            ex.run(acc, a, w, I, adapters, lds, lane);
 
         auto step = [&](const StepW4<G> &s, int i) {
             const int t = sb - p0 + i;
-            main_step<1, G, kZeros>(acc, s, decode, 1, frag + t * kStepChunks * kWave, xs + t * kXs, lane);
+            main_step<1, 1, G, kZeros>(acc, s, decode, frag + t * kStepChunks * kWave, xs + t * kXs, lane);
         };
         int i0 = 0;
         for (; i0 + D < ns; i0 += D) {
@@ -146,16 +138,13 @@ __global__ __launch_bounds__(NW * kWave, W4_W) void expert_gemm_w4_kernel(GemmW4
         store_slab<1, kGated>(acc, a, row0, n_rows, w.slab, lane);
 }
 
-#ifndef W4_KS
-#define W4_KS 2048
-#endif
 // Shares of K per slab: 1 when the slabs alone make two waves per SIMD,
 // doubling until they do or a share has no step left.
 int k_shares_log(const GemmW4Args &a)
 {
     const long long slabs = (long long)std::min(a.n_tiles, a.n_busy) * a.n_slabs;
     int log = 0;
-    while (log < 3 && (slabs << log) < W4_KS && (a.k_units / 2 >> (log + 1)) >= 1)
+    while (log < 3 && (slabs << log) < 2048 && (a.k_units / 2 >> (log + 1)) >= 1)
         ++log;
     return log;
 }
@@ -165,7 +154,7 @@ hipError_t launch_few(const GemmW4Args &a, int log, hipStream_t s)
 {
     const int WN = NW >> log;
     const int blocks = (a.n_tiles * ((a.n_slabs + WN - 1) / WN) + 7) / 8 * 8;
-    const int staged = std::min(kPanelSteps, a.k_units / 2) * step_lds_bytes(1, G) +
+    const int staged = std::min(panel_steps(NW), a.k_units / 2) * step_lds_bytes(1, G) +
                        (a.S ? (a.r + 31) / 32 * 1024 : 0);
     const int parts = log ? (NW - WN) * kNS * kWave * 16 : 0;
     hipLaunchKernelGGL((expert_gemm_w4_kernel<NW, G, kGated, kZeros>), dim3(blocks), dim3(NW * kWave),

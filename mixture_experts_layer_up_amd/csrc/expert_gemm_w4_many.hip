@@ -18,37 +18,23 @@
 namespace moe_lora {
 namespace {
 
-template <int MT, int G, bool kGated, bool kZeros>
-__global__ __launch_bounds__(256, MT == 4 ? 2 : 3) void expert_gemm_w4_many_kernel(GemmW4Args a, int per)
+constexpr int kMinBlocks = 1024;  // two rounds of two blocks per CU
+
+// A block's share: what the whole block agrees on.
+struct Job {
+    int le, row0, n_rows, sg0, sg1;
+};
+
+// The block's work with NM of its MT row tiles (rows behind n_rows repeat the
+// last one and are not stored).
+template <int NM, int MT, int G, bool kGated, bool kZeros>
+__device__ __forceinline__ void run_job(const GemmW4Args &a, const Job &job, u32x4 *lds, int wave, int lane)
 {
     constexpr int kUnit = kStepChunks * MT * kWave;  // fragments of a step (16-byte pieces)
     constexpr int kXs = 128 / G * MT * 16;           // its group sums
     constexpr int SB = 4 / MT;                       // steps staged together: a unit per wave
-    extern __shared__ u32x4 lds[];  // two buffers of SB steps, their group sums, S fragments
-    const int lane = threadIdx.x & (kWave - 1);
-    const int wave = wave_id();
-    const int n_sg = (a.n_slabs + 3) / 4;
-    const int n_jobs = (n_sg + per - 1) / per;
-
-    const int logical = xcd_balanced_item(blockIdx.x, n_tiles_used(a) * n_jobs);
-    if (logical < 0)
-        return;
-    const TileW4 te = find_tile(a, logical / n_jobs);
-    const int le = te.le;
-    if (le < 0)
-        return;
-    // the row tiles of one job are neighbours and share its codes in L2; an
-    // expert's rows are cut evenly
-    const int nt = (te.rows + a.tile_rows - 1) / a.tile_rows;
-    const int in_expert = logical - te.first * n_jobs;
-    const int job = in_expert / nt;
-    const int sub = in_expert - job * nt;
-    const int rows_per = ((te.rows + nt - 1) / nt + 15) & ~15;
-    const int row0 = te.row + sub * rows_per;
-    const int n_rows = min(rows_per, te.rows - sub * rows_per);
-    const int n_mt = (n_rows + 15) >> 4;
+    constexpr int kExpandSteps = MT == 4 ? 2 : 4;    // in flight: what the registers hold
     const int I = kGated ? a.I : 0;
-    const int sg0 = job * per, sg1 = min(n_sg, sg0 + per);
     const int n_steps = a.k_units / 2;
     const int n_pairs = (n_steps + 1) / 2;
 
@@ -57,8 +43,8 @@ __global__ __launch_bounds__(256, MT == 4 ? 2 : 3) void expert_gemm_w4_many_kern
     u32x4 *sfrag = reinterpret_cast<u32x4 *>(xs + 2 * SB * kXs);
     const DecodeW4 decode;
 
-    auto slab_of = [&](int sg) { return find_slab(a, le, min(sg * 4 + wave, a.n_slabs - 1)); };
-    SlabW4 w = slab_of(sg0);
+    auto slab_of = [&](int sg) { return find_slab(a, job.le, min(sg * 4 + wave, a.n_slabs - 1)); };
+    SlabW4 w = slab_of(job.sg0);
     StepW4<G> st[2];
     load_step<G, kZeros>(st[0], a, w, 0, lane);
     load_step<G, kZeros>(st[1], a, w, min(1, n_steps - 1), lane);
@@ -70,7 +56,7 @@ __global__ __launch_bounds__(256, MT == 4 ? 2 : 3) void expert_gemm_w4_many_kern
     uint32_t adapters = 0xffffffffu;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-        const int p = row0 + min(m * 16 + (lane & 15), n_rows - 1);
+        const int p = job.row0 + min(m * 16 + (lane & 15), job.n_rows - 1);
         const uint32_t l = find_row<kGated>(a, p, um == m, &arow, &slot);
         adapters = (adapters & ~(0xffu << (8 * m))) | (l << (8 * m));
     }
@@ -80,26 +66,24 @@ __global__ __launch_bounds__(256, MT == 4 ? 2 : 3) void expert_gemm_w4_many_kern
     const int s_chunks = a.S ? (a.r + 31) >> 5 : 0;
     for (int c = uh; c < s_chunks; c += SB)
         sfrag[(c * MT + um) * kWave + lane] = load_s(a, slot, c, lane);
-    auto stage = [&](int buf) {
-        store_unit<MT, G>(v, frag + (buf * SB + uh) * kUnit + um * kWave, xs + (buf * SB + uh) * kXs + um * 16,
+    auto stage = [&](int buf, int step) {
+        store_unit<MT, G, kZeros>(v, step, a.K, frag + (buf * SB + uh) * kUnit + um * kWave, xs + (buf * SB + uh) * kXs + um * 16,
                           lane);
     };
-    stage(0);
+    stage(0, uh);
     lds_barrier();
-    const unsigned long long used = a.S ? adapters_used(adapters, n_mt) : 0;
+    const unsigned long long used = a.S ? adapters_used(adapters, NM) : 0;
 
-    f32x4 acc[MT][kNS];
+    f32x4 acc[NM][kNS];
     zero_acc(acc);
     auto compute = [&](const StepW4<G> &s, int b) {  // b: step buffer 0 .. 2 SB - 1
-        main_step<MT, G, kZeros>(acc, s, decode, n_mt, frag + b * kUnit, xs + b * kXs, lane);
+        main_step<NM, MT, G, kZeros>(acc, s, decode, frag + b * kUnit, xs + b * kXs, lane);
     };
     int buf = 0;  // SB == 2: buffer of the current pair
-    for (int sg = sg0; sg < sg1; ++sg) {
-        const SlabW4 wn = slab_of(min(sg + 1, sg1 - 1));
-        unsigned long long left = used;
-        ExpandStep e{-1, 0};
-        u32x4 eb[kNS];
+    for (int sg = job.sg0; sg < job.sg1; ++sg) {
+        const SlabW4 wn = slab_of(min(sg + 1, job.sg1 - 1));
         for (int p = 0; p < n_pairs; ++p) {
+            // behind its last pair the ring goes on with the next slab
             const bool last = p + 1 == n_pairs;
             const SlabW4 wl = last ? wn : w;
             const int next = last ? 0 : 2 * p + 2;
@@ -110,38 +94,73 @@ __global__ __launch_bounds__(256, MT == 4 ? 2 : 3) void expert_gemm_w4_many_kern
                 if (2 * p + 1 < n_steps)
                     compute(st[1], buf * 2 + 1);
                 load_step<G, kZeros>(st[1], a, wl, min(next + 1, n_steps - 1), lane);
-                stage(buf ^ 1);
+                stage(buf ^ 1, next + uh);
                 lds_barrier();
                 buf ^= 1;
             } else {
                 load_unit(v, arow, 2 * p + 1, a.K);
                 compute(st[0], 0);
                 load_step<G, kZeros>(st[0], a, wl, next, lane);
-                stage(1);
+                stage(1, 2 * p + 1);
                 lds_barrier();
                 load_unit(v, arow, next, a.K);
                 if (2 * p + 1 < n_steps)
                     compute(st[1], 1);
                 load_step<G, kZeros>(st[1], a, wl, min(next + 1, n_steps - 1), lane);
-                stage(0);
+                stage(0, next);
                 lds_barrier();
             }
         }
-        if (left) {
-            e = next_expand(e, &left, a.r);
-            load_expand(eb, a, w, e, I, lane);
-            expand_all<MT>(acc, eb, e, left, a, w, I, adapters, n_mt, sfrag, lane);
+        if (used) {
+            Expand<NM, MT, kExpandSteps> ex;
+            ex.start(used, a, w, I, lane);
+            ex.run(acc, a, w, I, adapters, sfrag, lane);
         }
         if (sg * 4 + wave < a.n_slabs)
-            store_slab<MT, kGated>(acc, a, row0, n_rows, w.slab, lane);
+            store_slab<NM, kGated>(acc, a, job.row0, job.n_rows, w.slab, lane);
         zero_acc(acc);
         w = wn;
+        // No store may be outstanding in the loop above: the compiler would have
+        // to wait for all loads wherever it waits for one.
+        __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
     }
 }
 
-#ifndef W4_BLOCKS
-#define W4_BLOCKS 1024
-#endif
+template <int MT, int G, bool kGated, bool kZeros>
+__global__ __launch_bounds__(256, 2) void expert_gemm_w4_many_kernel(GemmW4Args a, int per)
+{
+    extern __shared__ u32x4 lds[];  // two buffers of SB steps, their group sums, S fragments
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = wave_id();
+    const int n_sg = (a.n_slabs + 3) / 4;
+    const int n_jobs = (n_sg + per - 1) / per;
+
+    const int logical = xcd_balanced_item(blockIdx.x, n_tiles_used(a) * n_jobs);
+    if (logical < 0)
+        return;
+    const TileW4 te = find_tile(a, logical / n_jobs);
+    if (te.le < 0)
+        return;
+    // the row tiles of one job are neighbours and share its codes in L2; an
+    // expert's rows are cut evenly
+    const int nt = (te.rows + a.tile_rows - 1) / a.tile_rows;
+    const int in_expert = logical - te.first * n_jobs;
+    const int at = in_expert / nt;
+    const int sub = in_expert - at * nt;
+    const int rows_per = ((te.rows + nt - 1) / nt + 15) & ~15;
+    const Job job{te.le, te.row + sub * rows_per, min(rows_per, te.rows - sub * rows_per), at * per,
+                  min(n_sg, at * per + per)};
+    const int n_mt = (job.n_rows + 15) >> 4;
+    if (MT == 4 && n_mt <= 2)
+        run_job<2, MT, G, kGated, kZeros>(a, job, lds, wave, lane);
+    else if (MT == 4 && n_mt == 3)
+        run_job<MT == 4 ? 3 : 1, MT, G, kGated, kZeros>(a, job, lds, wave, lane);
+    else if (MT == 2 && n_mt == 1)
+        run_job<1, MT, G, kGated, kZeros>(a, job, lds, wave, lane);
+    else
+        run_job<MT, MT, G, kGated, kZeros>(a, job, lds, wave, lane);
+}
+
 template <int MT, int G, bool kGated, bool kZeros>
 hipError_t launch_many(const GemmW4Args &a, hipStream_t s)
 {
@@ -149,7 +168,7 @@ hipError_t launch_many(const GemmW4Args &a, hipStream_t s)
     // slab groups per block: as many as still leave that many blocks
     const int tiles = std::min(a.n_tiles, std::max(a.n_busy, a.n_slots / a.tile_rows));
     int per = 1;
-    while (per < n_sg && (long long)tiles * ((n_sg + per) / (per + 1)) >= W4_BLOCKS)
+    while (per < n_sg && (long long)tiles * ((n_sg + per) / (per + 1)) >= kMinBlocks)
         ++per;
     const int blocks = (a.n_tiles * ((n_sg + per - 1) / per) + 7) / 8 * 8;
     const int lds = 2 * (4 / MT) * step_lds_bytes(MT, G) + (a.S ? (a.r + 31) / 32 * MT * 1024 : 0);

@@ -175,23 +175,29 @@ __device__ __forceinline__ void fix_expand(u32x4 (&b)[kNS], const GemmW4Args &a,
 }
 
 // The activations of one step and row tile: four A fragments, loaded from the
-// lane's row (at its K quarter) and 0 behind K.
+// lane's row (at its K quarter; behind K the row's end again).
 __device__ __forceinline__ void load_unit(u32x4 (&v)[kStepChunks], const uint16_t *row, int step, int K)
 {
 #pragma unroll
-    for (int c = 0; c < kStepChunks; ++c) {
-        const int k0 = step * 128 + c * 32;
-        v[c] = keep_if(load16(row + min(k0, K - 32)), k0 < K);
-    }
+    for (int c = 0; c < kStepChunks; ++c)
+        v[c] = load16(row + min(step * 128 + c * 32, K - 32));
 }
 
-// Stores them to LDS with their group sums: frag[chunk * MT][lane], and per
-// group the 16 rows' sums at xs[group * MT * 16].  The sums come from MFMAs
-// against ones, whose every column is the row's sum.
-template <int MT, int G>
-__device__ __forceinline__ void store_unit(const u32x4 (&v)[kStepChunks], u32x4 *frag, float *xs, int lane)
+// Stores them to LDS, 0 behind K, with their group sums: frag[chunk * MT][lane],
+// and per group the 16 rows' -sum (times 24 = 16 + z in formats without zero
+// points) at xs[group * MT * 16].  The sums come from MFMAs against ones, whose
+// every column is the row's sum.  (The clearing is here and not at the load,
+// which it would make wait.)
+template <int MT, int G, bool kZeros>
+__device__ __forceinline__ void store_unit(u32x4 (&v)[kStepChunks], int step, int K, u32x4 *frag, float *xs,
+                                           int lane)
 {
     const u32x4 ones{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+    if (step * 128 + 128 > K) {
+#pragma unroll
+        for (int c = 0; c < kStepChunks; ++c)
+            v[c] = keep_if(v[c], step * 128 + c * 32 < K);
+    }
 #pragma unroll
     for (int c = 0; c < kStepChunks; ++c)
         frag[c * MT * kWave + lane] = v[c];
@@ -202,51 +208,59 @@ __device__ __forceinline__ void store_unit(const u32x4 (&v)[kStepChunks], u32x4 
         for (int i = 0; i < G / 32; ++i)
             sum = mfma_16x16x32(v[g * (G / 32) + i], ones, sum);
         if ((lane & 15) == 0)
-            *reinterpret_cast<f32x4 *>(xs + g * MT * 16 + (lane >> 4) * 4) = sum;
+            *reinterpret_cast<f32x4 *>(xs + g * MT * 16 + (lane >> 4) * 4) = sum * (kZeros ? -1.0f : -24.0f);
     }
 }
 
-// A main step: per group, MFMAs over its chunks into fresh accumulators, then
-// acc += s (grp - (16 + z) xs).  frag and xs as store_unit left them.
-template <int MT, int G, bool kZeros>
-__device__ __forceinline__ void main_step(f32x4 (&acc)[MT][kNS], const StepW4<G> &st, const DecodeW4 &decode,
-                                          int n_mt, const u32x4 *frag, const float *xs, int lane)
+// A main step over NM of the MT staged row tiles: per group, MFMAs over its
+// chunks into accumulators that start from -(16 + z) xs, then acc += s grp.
+// frag and xs as store_unit left them.  NM is a constant: a branch around a
+// row tile would keep the LDS reads from running ahead of the MFMAs.  With
+// more than two row tiles the columns go in two halves, each reading the
+// fragments again: the group's accumulators then need half the registers.
+template <int NM, int MT, int G, bool kZeros>
+__device__ __forceinline__ void main_step(f32x4 (&acc)[NM][kNS], const StepW4<G> &st, const DecodeW4 &decode,
+                                          const u32x4 *frag, const float *xs, int lane)
 {
     constexpr int kGroupChunks = G / 32;
-    const f32x4 zero{0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int NN = NM > 2 ? 2 : 4;  // column tiles at a time
 #pragma unroll
     for (int g = 0; g < StepW4<G>::kGroups; ++g) {
-        f32x4 grp[MT][kNS];
-#pragma unroll
-        for (int i = 0; i < kGroupChunks; ++i) {
-            const int c = g * kGroupChunks + i;
-            u32x4 b[kNS];
-#pragma unroll
-            for (int n = 0; n < kNS; ++n)
-                b[n] = decode(st.b[(c >> 1) * 2 + (n >> 1)][(n & 1) * 2 + (c & 1)]);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if (m < n_mt) {
-                    const u32x4 v = frag[(c * MT + m) * kWave + lane];
-#pragma unroll
-                    for (int n = 0; n < kNS; ++n)
-                        grp[m][n] = mfma_16x16x32(v, b[n], i == 0 ? zero : grp[m][n]);
-                }
-            }
-        }
         const uint2 sc = st.sc[g];
         const float s[kNS] = {__uint_as_float(sc.x << 16), __uint_as_float(sc.x & 0xffff0000u),
                               __uint_as_float(sc.y << 16), __uint_as_float(sc.y & 0xffff0000u)};
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            if (m < n_mt) {
-                const f32x4 sum = *reinterpret_cast<const f32x4 *>(xs + (g * MT + m) * 16 + (lane >> 4) * 4);
+        for (int n0 = 0; n0 < kNS; n0 += NN) {
+            f32x4 grp[NM][NN], sum[NM];
 #pragma unroll
-                for (int n = 0; n < kNS; ++n) {
-                    const float c = kZeros ? (float)((st.zr[g] >> (8 * n)) & 0xffu) : 24.0f;
+            for (int m = 0; m < NM; ++m)
+                sum[m] = *reinterpret_cast<const f32x4 *>(xs + (g * MT + m) * 16 + (lane >> 4) * 4);
+#pragma unroll
+            for (int i = 0; i < kGroupChunks; ++i) {
+                const int c = g * kGroupChunks + i;
+                u32x4 x[NM];
+#pragma unroll
+                for (int m = 0; m < NM; ++m)
+                    x[m] = frag[(c * MT + m) * kWave + lane];
+#pragma unroll
+                for (int n = 0; n < NN; ++n) {
+                    const u32x4 b = decode(st.b[(c >> 1) * 2 + ((n0 + n) >> 1)][(n & 1) * 2 + (c & 1)]);
+                    const float z = kZeros ? (float)((st.zr[g] >> (8 * (n0 + n))) & 0xffu) : 1.0f;
+#pragma unroll
+                    for (int m = 0; m < NM; ++m)
+                        grp[m][n] = mfma_16x16x32(x[m], b, i > 0 ? grp[m][n] : kZeros ? sum[m] * z : sum[m]);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NN; ++n) {
+#pragma unroll
+                for (int m = 0; m < NM; ++m) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        acc[m][n][i] = fmaf(s[n], fmaf(-c, sum[i], grp[m][n][i]), acc[m][n][i]);
+                        acc[m][n0 + n][i] = fmaf(s[n0 + n], grp[m][n][i], acc[m][n0 + n][i]);
+                    // the sums are made here: sunk to their use in a later step,
+                    // they would keep the group's accumulators alive
+                    asm volatile("" : "+v"(acc[m][n0 + n]));
                 }
             }
         }
@@ -286,49 +300,56 @@ __device__ __forceinline__ ExpandStep next_expand(ExpandStep e, unsigned long lo
     return ExpandStep{l, 0};
 }
 
-// An expand step; x(m): the S fragment of its rank positions.
-template <int MT, typename LoadA>
-__device__ __forceinline__ void expand_step(f32x4 (&acc)[MT][kNS], const u32x4 (&b)[kNS], ExpandStep e,
-                                            uint32_t adapters, int n_mt, LoadA x)
-{
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        if (m < n_mt) {
-            const u32x4 v = keep_if(x(m), ((adapters >> (8 * m)) & 0xffu) == (uint32_t)e.l);
-#pragma unroll
-            for (int n = 0; n < kNS; ++n)
-                acc[m][n] = mfma_16x16x32(v, b[n], acc[m][n]);
+// The whole expand of a wave, over NM of MT row tiles, with NE steps' operands
+// in flight: the steps of `used` adapters in order, each its rank positions.
+template <int NM, int MT, int NE>
+struct Expand {
+    unsigned long long used;
+    ExpandStep at;      // the next one to load, l < 0: none
+    ExpandStep e[NE];
+    u32x4 b[NE][kNS];
+
+    __device__ __forceinline__ void load(int i, const GemmW4Args &a, const SlabW4 &w, int I, int lane)
+    {
+        e[i] = at;
+        if (at.l >= 0) {  // uniform
+            load_expand(b[i], a, w, at, I, lane);
+            at = next_expand(at, &used, a.r);
         }
     }
-}
-
-// The whole expand of a wave: e is the first step, its operands in b; two
-// steps' loads are in flight.  sfrag: S fragments [rank chunk][m][lane].
-template <int MT>
-__device__ __forceinline__ void expand_all(f32x4 (&acc)[MT][kNS], u32x4 (&b)[kNS], ExpandStep e,
-                                           unsigned long long used, const GemmW4Args &a, const SlabW4 &w,
-                                           int I, uint32_t adapters, int n_mt, const u32x4 *sfrag, int lane)
-{
-    auto step = [&](u32x4(&v)[kNS], ExpandStep now) {
-        if (a.r & 7)
-            fix_expand(v, a, w, now, I, lane);
-        expand_step<MT>(acc, v, now, adapters, n_mt, [&](int m) {
-            return sfrag[(now.q0 / 32 * MT + m) * kWave + lane];
-        });
-    };
-    u32x4 b2[kNS];
-    while (e.l >= 0) {  // uniform
-        const ExpandStep e2 = next_expand(e, &used, a.r);
-        if (e2.l >= 0)
-            load_expand(b2, a, w, e2, I, lane);
-        step(b, e);
-        e = e2.l >= 0 ? next_expand(e2, &used, a.r) : e2;
-        if (e.l >= 0)
-            load_expand(b, a, w, e, I, lane);
-        if (e2.l >= 0)
-            step(b2, e2);
+    __device__ __forceinline__ void start(unsigned long long adapters, const GemmW4Args &a, const SlabW4 &w,
+                                          int I, int lane)
+    {
+        used = adapters;
+        at = next_expand(ExpandStep{-1, 0}, &used, a.r);
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            load(i, a, w, I, lane);
     }
-}
+    // sfrag: S fragments [rank chunk][m][lane]
+    __device__ __forceinline__ void run(f32x4 (&acc)[NM][kNS], const GemmW4Args &a, const SlabW4 &w, int I,
+                                        uint32_t adapters, const u32x4 *sfrag, int lane)
+    {
+        while (e[0].l >= 0) {
+#pragma unroll
+            for (int i = 0; i < NE; ++i) {
+                if (e[i].l < 0)
+                    continue;
+                if (a.r & 7)
+                    fix_expand(b[i], a, w, e[i], I, lane);
+#pragma unroll
+                for (int m = 0; m < NM; ++m) {
+                    const u32x4 v = keep_if(sfrag[(e[i].q0 / 32 * MT + m) * kWave + lane],
+                                            ((adapters >> (8 * m)) & 0xffu) == (uint32_t)e[i].l);
+#pragma unroll
+                    for (int n = 0; n < kNS; ++n)
+                        acc[m][n] = mfma_16x16x32(v, b[i][n], acc[m][n]);
+                }
+                load(i, a, w, I, lane);
+            }
+        }
+    }
+};
 
 // The lane's row of row tile m of a tile: the adapter (0xff: none), and the
 // activation row and slot where `mine`.
@@ -361,32 +382,36 @@ __device__ __forceinline__ u32x4 load_s(const GemmW4Args &a, int slot, int chunk
 // Writes a wave's 64 columns of a tile from its accumulators: lane l holds
 // rows 4 (l / 16) + i of column l % 16, and gate and up of a column sit in
 // neighbouring tiles of the same lane.
-template <int MT, bool kGated>
-__device__ __forceinline__ void store_slab(const f32x4 (&acc)[MT][kNS], const GemmW4Args &a, int row0,
+template <int NM, bool kGated>
+__device__ __forceinline__ void store_slab(const f32x4 (&acc)[NM][kNS], const GemmW4Args &a, int row0,
                                            int n_rows, int slab, int lane)
 {
+    asm("" : "+v"(lane));  // addresses are made here, not kept through the main loop
+    const int width = kGated ? a.I : a.n_canon;
+    const size_t base = (size_t)row0 * width + slab * (kGated ? 32 : 64);  // uniform
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int m = 0; m < NM; ++m) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = m * 16 + (lane >> 4) * 4 + i;
-            if (row >= n_rows)
-                continue;
-            if (kGated) {
-                uint16_t *y = static_cast<uint16_t *>(a.Y) + (size_t)(row0 + row) * a.I + slab * 32 + (lane & 15);
+            const size_t at = base + (size_t)(unsigned)row * width + (lane & 15);
+            if (row < n_rows) {
+                if (kGated) {
+                    uint16_t *y = static_cast<uint16_t *>(a.Y) + at;
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    y[j * 16] = (uint16_t)float_to_bf16_bits(silu_f32(acc[m][2 * j][i]) * acc[m][2 * j + 1][i]);
-            } else {
-                const size_t at = (size_t)(row0 + row) * a.n_canon + slab * 64 + (lane & 15);
+                    for (int j = 0; j < 2; ++j)
+                        y[j * 16] = (uint16_t)float_to_bf16_bits(silu_f32(acc[m][2 * j][i]) * acc[m][2 * j + 1][i]);
+                } else if (a.y_f32) {
 #pragma unroll
-                for (int n = 0; n < kNS; ++n) {
-                    if (a.y_f32)
+                    for (int n = 0; n < kNS; ++n)
                         static_cast<float *>(a.Y)[at + n * 16] = acc[m][n][i];
-                    else
+                } else {
+#pragma unroll
+                    for (int n = 0; n < kNS; ++n)
                         static_cast<uint16_t *>(a.Y)[at + n * 16] = (uint16_t)float_to_bf16_bits(acc[m][n][i]);
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 }
