@@ -116,7 +116,7 @@ Layout make_layout(const moe_lora_shape *s, const moe_lora_w4_format *w4 = nullp
     L.seg_offsets = take((segs + 1) * 4);
     L.seg_slots = take(n * 4);
     L.perm_scratch = take(permute_scratch_bytes((int)n, (int)el, s->num_loras));
-    L.tile_rows = w4 ? gemm_w4_tile_rows((int)n, (int)el)
+    L.tile_rows = w4 ? gemm_w4_tile_rows((int)n, s->num_experts, (int)el)
                      : gemm_tile_rows((int)n, (int)el, s->hidden, s->inter,
                                       lora_gate_up_active(s) ? s->rank_gate_up : 0,
                                       lora_down_active(s) ? s->rank_down : 0);

@@ -60,8 +60,8 @@ struct FinalizeF32Args {
     float scale;
 };
 
-// Rows per work-list tile for n slots over E_l local experts.
-int gemm_w4_tile_rows(int n_slots, int E_l);
+// Rows per work-list tile (16, 32 or 64) for n slots over E experts, E_l of them local.
+int gemm_w4_tile_rows(int n_slots, int E, int E_l);
 hipError_t launch_gemm_w4(const GemmW4Args &a, bool gated, hipStream_t s);
 hipError_t launch_gemm_w4_many(const GemmW4Args &a, bool gated, hipStream_t s);  // tiles of 32, 64 rows
 hipError_t launch_finalize_f32(const FinalizeF32Args &a, hipStream_t s);
