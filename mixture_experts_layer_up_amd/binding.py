@@ -179,6 +179,11 @@ def _ptr(t: Optional[torch.Tensor], dtype=None, shape: Optional[Sequence[int]] =
          name: str = "tensor"):
     if t is None:
         return None
+    # the good case first: a small batch's kernels take as long as these checks
+    if (t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype is dtype or
+                                              (dtype.__class__ is tuple and t.dtype in dtype))
+            and (shape is None or t.shape == shape)):
+        return t.data_ptr()
     if not t.is_cuda:
         raise MoELoRAError(f"{name} must be a device tensor")
     if not t.is_contiguous():
@@ -413,26 +418,26 @@ def finalize(shape: Shape, expert_out: torch.Tensor, routing: Dict[str, torch.Te
     return out
 
 
-class _on:
-    """The device that holds every given tensor, made current; its current stream."""
+def _one_gpu(*tensors) -> int:
+    """Index of the one GPU that holds every given tensor."""
+    index = -1
+    for t in tensors:
+        if t is not None and (i := t.get_device()) != index:
+            if index >= 0 or i < 0:
+                raise MoELoRAError("tensors must be on one GPU, got "
+                                   f"{sorted({str(x.device) for x in tensors if x is not None})}")
+            index = i
+    if index < 0:
+        raise MoELoRAError("no tensor given")
+    return index
 
-    def __init__(self, *tensors):
-        devices = {t.device for t in tensors if t is not None}
-        if len(devices) != 1 or next(iter(devices)).type != "cuda":
-            raise MoELoRAError(f"tensors must be on one GPU, got {sorted(map(str, devices))}")
-        self.device = devices.pop()
-        self.stream = torch.cuda.current_stream(self.device).cuda_stream
-        self.guard = None
 
-    def __enter__(self):
-        if self.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _on(index: int, call):
+    """call(current stream of GPU `index`) with that GPU current."""
+    if index == torch.cuda.current_device():
+        return call(torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
+        return call(torch._C._cuda_getCurrentRawStream(index))
 
 
 def workspace_size_w4(shape: Shape, fmt: W4Format) -> int:
@@ -466,17 +471,17 @@ def quantize_w4(shape: Shape, fmt: W4Format, w13: torch.Tensor, w2: torch.Tensor
     """4-bit weights of w13 [E_l, H, 2I] and w2 [E_l, I, H] (bf16): two dicts of
     ``codes``, ``scales`` and ``zeros`` (None without zero points)."""
     E_l, H, I = shape.local_num_experts, shape.hidden, shape.inter
-    with _on(w13, w2) as stream:
-        out = []
-        for which in (0, 1):
-            codes, groups = w4_shapes(shape, fmt, which)
-            new = lambda s, dt: torch.empty(s, dtype=dt, device=w13.device)  # noqa: E731
-            out.append({"codes": new(codes, torch.uint8), "scales": new(groups, torch.bfloat16),
-                        "zeros": new(groups, torch.uint8) if fmt.zero_points else None})
-        _check(load_library().moe_lora_quantize_w4(
-            ctypes.byref(shape), ctypes.byref(fmt), _ptr(w13, _BF16, (E_l, H, 2 * I), "w13"),
+    gpu = _one_gpu(w13, w2)
+    out = []
+    for which in (0, 1):
+        codes, groups = w4_shapes(shape, fmt, which)
+        new = lambda s, dt: torch.empty(s, dtype=dt, device=w13.device)  # noqa: E731
+        out.append({"codes": new(codes, torch.uint8), "scales": new(groups, torch.bfloat16),
+                    "zeros": new(groups, torch.uint8) if fmt.zero_points else None})
+    args = (ctypes.byref(shape), ctypes.byref(fmt), _ptr(w13, _BF16, (E_l, H, 2 * I), "w13"),
             _ptr(w2, _BF16, (E_l, I, H), "w2"), ctypes.byref(_w4_struct(shape, fmt, 0, out[0])),
-            ctypes.byref(_w4_struct(shape, fmt, 1, out[1])), stream))
+            ctypes.byref(_w4_struct(shape, fmt, 1, out[1])))
+    _check(_on(gpu, lambda stream: load_library().moe_lora_quantize_w4(*args, stream)))
     return out[0], out[1]
 
 
@@ -485,13 +490,13 @@ def pack_weights_w4(shape: Shape, fmt: W4Format, w13: Dict, w2: Dict):
     of ``codes``, ``scales`` and ``zeros`` (:func:`quantize_w4`)."""
     lib = load_library()
     every = [q.get(n) for q in (w13, w2) for n in ("codes", "scales", "zeros")]
-    with _on(*every) as stream:
-        s13, s2 = _w4_struct(shape, fmt, 0, w13), _w4_struct(shape, fmt, 1, w2)
-        p13, p2 = (torch.empty(packed_w4_bytes(shape, fmt, which), dtype=torch.uint8,
-                               device=w13["codes"].device) for which in (0, 1))
-        _check(lib.moe_lora_pack_weights_w4(
-            ctypes.byref(shape), ctypes.byref(fmt), ctypes.byref(s13), ctypes.byref(s2),
-            p13.data_ptr(), p2.data_ptr(), stream))
+    gpu = _one_gpu(*every)
+    s13, s2 = _w4_struct(shape, fmt, 0, w13), _w4_struct(shape, fmt, 1, w2)
+    p13, p2 = (torch.empty(packed_w4_bytes(shape, fmt, which), dtype=torch.uint8,
+                           device=w13["codes"].device) for which in (0, 1))
+    _check(_on(gpu, lambda stream: lib.moe_lora_pack_weights_w4(
+        ctypes.byref(shape), ctypes.byref(fmt), ctypes.byref(s13), ctypes.byref(s2),
+        p13.data_ptr(), p2.data_ptr(), stream)))
     return p13, p2
 
 
@@ -509,24 +514,24 @@ def forward_w4(shape: Shape, fmt: W4Format, hidden: torch.Tensor, w13_packed: to
     """:func:`forward` with 4-bit expert weights, packed by :func:`pack_weights_w4`
     for ``fmt``; the other arguments are those of :func:`forward`."""
     T, H = shape.num_tokens, shape.hidden
-    with _on(hidden, w13_packed, w2_packed, lora_a_gate_up, lora_b_gate_up, lora_a_down, lora_b_down,
-             token_lora_mapping, router_logits, topk_ids, topk_weights, routing_bias, out, workspace,
-             expert_out, input_flags, *(routing.values() if routing is not None else ())) as stream:
-        if out is None and expert_out is None:
-            out = torch.empty((T, H), dtype=torch.bfloat16, device=hidden.device)
-        inputs, _ev = _inputs(shape, hidden, w13_packed, w2_packed, lora_a_gate_up, lora_b_gate_up,
-                              lora_a_down, lora_b_down, token_lora_mapping, router_logits, topk_ids,
-                              topk_weights, routing_bias, stage_events, expert_out, side_stream,
-                              fork_event, join_event, input_flags, w4=fmt)
-        rs = _routing_struct(routing) if routing is not None else None
-        if workspace is None:
-            workspace = torch.empty(max(workspace_size_w4(shape, fmt), 1), dtype=torch.uint8,
-                                    device=hidden.device)
-        _check(load_library().moe_lora_forward_w4(
-            ctypes.byref(shape), ctypes.byref(fmt), ctypes.byref(inputs),
+    gpu = _one_gpu(hidden, w13_packed, w2_packed, lora_a_gate_up, lora_b_gate_up, lora_a_down,
+                   lora_b_down, token_lora_mapping, router_logits, topk_ids, topk_weights, routing_bias,
+                   out, workspace, expert_out, input_flags,
+                   *(routing.values() if routing is not None else ()))
+    if out is None and expert_out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=hidden.device)
+    inputs, _ev = _inputs(shape, hidden, w13_packed, w2_packed, lora_a_gate_up, lora_b_gate_up,
+                          lora_a_down, lora_b_down, token_lora_mapping, router_logits, topk_ids,
+                          topk_weights, routing_bias, stage_events, expert_out, side_stream,
+                          fork_event, join_event, input_flags, w4=fmt)
+    rs = _routing_struct(routing) if routing is not None else None
+    if workspace is None:
+        workspace = torch.empty(max(workspace_size_w4(shape, fmt), 1), dtype=torch.uint8,
+                                device=hidden.device)
+    args = (ctypes.byref(shape), ctypes.byref(fmt), ctypes.byref(inputs),
             ctypes.byref(rs) if rs is not None else None, _ptr(out, _BF16, (T, H), "out"),
-            _ptr(workspace, None, None, "workspace"),
-            workspace.numel() * workspace.element_size(), stream))
+            _ptr(workspace, None, None, "workspace"), workspace.numel() * workspace.element_size())
+    _check(_on(gpu, lambda stream: load_library().moe_lora_forward_w4(*args, stream)))
     return out
 
 
@@ -556,23 +561,23 @@ def balance_loss(shape: Shape, router_logits: torch.Tensor, topk_ids: torch.Tens
     :func:`route_backward` takes the result for the loss's gradient."""
     T, E, k = shape.num_tokens, shape.num_experts, shape.top_k
     lib = load_library()
-    with _on(router_logits, topk_ids, token_mask, seq_offsets, workspace) as stream:
-        tokens, S = _tokens(shape, token_mask, seq_offsets)
-        dev = router_logits.device
-        need = int(lib.moe_lora_balance_workspace_size(ctypes.byref(shape), S))
-        if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        r = {"loss": torch.empty(1, dtype=torch.float32, device=dev),
-             "counts": torch.empty((S, E), dtype=torch.int32, device=dev),
-             "probs": torch.empty((S, E), dtype=torch.float32, device=dev),
-             "tokens": torch.empty(S, dtype=torch.int32, device=dev)}
-        _check(lib.moe_lora_balance_loss(
-            ctypes.byref(shape), _ptr(router_logits, torch.float32, (T, E), "router_logits"),
+    gpu = _one_gpu(router_logits, topk_ids, token_mask, seq_offsets, workspace)
+    tokens, S = _tokens(shape, token_mask, seq_offsets)
+    dev = router_logits.device
+    need = int(lib.moe_lora_balance_workspace_size(ctypes.byref(shape), S))
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    r = {"loss": torch.empty(1, dtype=torch.float32, device=dev),
+         "counts": torch.empty((S, E), dtype=torch.int32, device=dev),
+         "probs": torch.empty((S, E), dtype=torch.float32, device=dev),
+         "tokens": torch.empty(S, dtype=torch.int32, device=dev)}
+    args = (ctypes.byref(shape), _ptr(router_logits, torch.float32, (T, E), "router_logits"),
             _ptr(topk_ids, torch.int32, (T, k), "topk_ids"), tokens,
             ctypes.byref(Balance(r["loss"].data_ptr(), r["counts"].data_ptr(),
                                  r["probs"].data_ptr(), r["tokens"].data_ptr())),
             _ptr(workspace, None, None, "workspace"),
-            workspace.numel() * workspace.element_size() if workspace is not None else 0, stream))
+            workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    _check(_on(gpu, lambda stream: lib.moe_lora_balance_loss(*args, stream)))
     return r
 
 
@@ -593,23 +598,23 @@ def route_backward(shape: Shape, router_logits: Optional[torch.Tensor],
     if (balance is None) != (d_loss is None):
         raise MoELoRAError("balance and d_loss are given together")
     kept = (balance["counts"], balance["tokens"]) if balance is not None else ()
-    with _on(router_logits, topk_ids, topk_weights, d_topk_weights, d_loss, token_mask, seq_offsets,
-             d_logits, *kept) as stream:
-        tokens, S = _tokens(shape, token_mask, seq_offsets)
-        bal = None
-        if balance is not None:
-            bal = ctypes.byref(Balance(None, _ptr(kept[0], torch.int32, (S, E), "counts"), None,
-                                       _ptr(kept[1], torch.int32, (S,), "tokens")))
-        if d_logits is None:
-            some = next(t for t in (router_logits, d_topk_weights, topk_ids) if t is not None)
-            d_logits = torch.empty((T, E), dtype=torch.float32, device=some.device)
-        _check(load_library().moe_lora_route_backward(
-            ctypes.byref(shape), _ptr(router_logits, torch.float32, (T, E), "router_logits"),
+    gpu = _one_gpu(router_logits, topk_ids, topk_weights, d_topk_weights, d_loss, token_mask,
+                   seq_offsets, d_logits, *kept)
+    tokens, S = _tokens(shape, token_mask, seq_offsets)
+    bal = None
+    if balance is not None:
+        bal = ctypes.byref(Balance(None, _ptr(kept[0], torch.int32, (S, E), "counts"), None,
+                                   _ptr(kept[1], torch.int32, (S,), "tokens")))
+    if d_logits is None:
+        some = next(t for t in (router_logits, d_topk_weights, topk_ids) if t is not None)
+        d_logits = torch.empty((T, E), dtype=torch.float32, device=some.device)
+    args = (ctypes.byref(shape), _ptr(router_logits, torch.float32, (T, E), "router_logits"),
             _ptr(topk_ids, torch.int32, (T, k), "topk_ids"),
             _ptr(topk_weights, torch.float32, (T, k), "topk_weights"),
             _ptr(d_topk_weights, torch.float32, (T, k), "d_topk_weights"), tokens, bal,
             _ptr(d_loss, torch.float32, (1,), "d_loss"),
-            _ptr(d_logits, torch.float32, (T, E), "d_logits"), stream))
+            _ptr(d_logits, torch.float32, (T, E), "d_logits"))
+    _check(_on(gpu, lambda stream: load_library().moe_lora_route_backward(*args, stream)))
     return d_logits
 
 
@@ -626,22 +631,22 @@ def finalize_backward(shape: Shape, d_out: torch.Tensor, expert_out: Optional[to
     T, H, k = shape.num_tokens, shape.hidden, shape.top_k
     perm = routing["expanded_idx_to_permuted_idx"]
     w = topk_weights if topk_weights is not None else routing.get("topk_weights")
-    with _on(d_out, expert_out, perm, w, d_expert_out, d_topk_weights) as stream:
-        if expert_out_grad and d_expert_out is None:
-            d_expert_out = torch.empty((T * k, H), dtype=torch.bfloat16, device=d_out.device)
-        if weights_grad and d_topk_weights is None:
-            d_topk_weights = torch.empty((T, k), dtype=torch.float32, device=d_out.device)
-        if not expert_out_grad:
-            d_expert_out = None
-        if not weights_grad:
-            d_topk_weights = None
-        _check(load_library().moe_lora_finalize_backward(
-            ctypes.byref(shape), _ptr(d_out, _BF16, (T, H), "d_out"),
+    gpu = _one_gpu(d_out, expert_out, perm, w, d_expert_out, d_topk_weights)
+    if not expert_out_grad:
+        d_expert_out = None
+    elif d_expert_out is None:
+        d_expert_out = torch.empty((T * k, H), dtype=torch.bfloat16, device=d_out.device)
+    if not weights_grad:
+        d_topk_weights = None
+    elif d_topk_weights is None:
+        d_topk_weights = torch.empty((T, k), dtype=torch.float32, device=d_out.device)
+    args = (ctypes.byref(shape), _ptr(d_out, _BF16, (T, H), "d_out"),
             _ptr(expert_out, _BF16, (T * k, H), "expert_out"),
             _ptr(perm, torch.int32, (T * k,), "expanded_idx_to_permuted_idx"),
             _ptr(w, torch.float32, (T, k), "topk_weights"),
             _ptr(d_expert_out, _BF16, (T * k, H), "d_expert_out"),
-            _ptr(d_topk_weights, torch.float32, (T, k), "d_topk_weights"), stream))
+            _ptr(d_topk_weights, torch.float32, (T, k), "d_topk_weights"))
+    _check(_on(gpu, lambda stream: load_library().moe_lora_finalize_backward(*args, stream)))
     return d_expert_out, d_topk_weights
 
 
