@@ -138,13 +138,13 @@ __global__ __launch_bounds__(NW * kWave, 3) void expert_gemm_w4_kernel(GemmW4Arg
         store_slab<1, kGated>(acc, a, row0, n_rows, w.slab, lane);
 }
 
-// Shares of K per slab: 1 when the slabs alone make two waves per SIMD,
+// Shares of K per slab: 1 when the slabs alone make a wave per SIMD,
 // doubling until they do or a share has no step left.
 int k_shares_log(const GemmW4Args &a)
 {
     const long long slabs = (long long)std::min(a.n_tiles, a.n_busy) * a.n_slabs;
     int log = 0;
-    while (log < 3 && (slabs << log) < 2048 && (a.k_units / 2 >> (log + 1)) >= 1)
+    while (log < 3 && (slabs << log) < 1024 && (a.k_units / 2 >> (log + 1)) >= 1)
         ++log;
     return log;
 }

@@ -37,34 +37,81 @@ __device__ __forceinline__ int seq_offset(const TokenSet &s, int i)
     return min(max(s.offsets[i], 0), s.T);
 }
 
-// First sequence that ends behind token t (S when there is none).
-__device__ __forceinline__ int seq_behind(const TokenSet &s, int t)
+// First sequence that ends behind token t (S when there is none), by a whole
+// wave: 64 offsets at a time instead of one per dependent load.
+__device__ __forceinline__ int seq_behind(const TokenSet &s, int t, int lane)
 {
-    int lo = 0, hi = s.S;
-    while (lo < hi) {
+    int lo = 0, hi = s.S;  // the answer lies in [lo, hi]
+    while (hi - lo > kWave) {
         const int mid = (lo + hi) >> 1;
-        if (seq_offset(s, mid + 1) > t)
+        if (__builtin_amdgcn_readfirstlane(seq_offset(s, mid + 1)) > t)
             hi = mid;
         else
             lo = mid + 1;
     }
-    return lo;
+    const bool behind = lo + lane < hi && seq_offset(s, lo + lane + 1) > t;
+    const unsigned long long m = __ballot(behind);
+    return m ? lo + __builtin_ctzll(m) : hi;
+}
+
+// Sum and maximum over a wave, the same value on every lane: row shifts and
+// broadcasts within the vector unit (a shuffle through LDS takes about ten
+// times as long, and these reductions are the kernels' dependent chain).
+template <int kCtrl, int kRows>
+__device__ __forceinline__ float dpp_move(float identity, float v)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(identity), __float_as_int(v), kCtrl, kRows,
+                                                     0xf, false));
+}
+
+__device__ __forceinline__ float last_lane(float v)
+{
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+    v += dpp_move<0x111, 0xf>(0.0f, v);  // from 1, 2, 4, 8 lanes below in the row of 16
+    v += dpp_move<0x112, 0xf>(0.0f, v);
+    v += dpp_move<0x114, 0xf>(0.0f, v);
+    v += dpp_move<0x118, 0xf>(0.0f, v);
+    v += dpp_move<0x142, 0xa>(0.0f, v);  // row ends into the next row
+    v += dpp_move<0x143, 0xc>(0.0f, v);  // lane 31 into the upper half
+    return last_lane(v);
 }
 
 __device__ __forceinline__ float wave_max(float v)
 {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1)
-        v = fmaxf(v, __shfl_xor(v, off));
-    return v;
+    const float low = -INFINITY;
+    v = fmaxf(v, dpp_move<0x111, 0xf>(low, v));
+    v = fmaxf(v, dpp_move<0x112, 0xf>(low, v));
+    v = fmaxf(v, dpp_move<0x114, 0xf>(low, v));
+    v = fmaxf(v, dpp_move<0x118, 0xf>(low, v));
+    v = fmaxf(v, dpp_move<0x142, 0xa>(low, v));
+    v = fmaxf(v, dpp_move<0x143, 0xc>(low, v));
+    return last_lane(v);
 }
 
-__device__ __forceinline__ float wave_sum(float v)
+__device__ __forceinline__ int wave_sum(int v)
 {
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1)
         v += __shfl_xor(v, off);
     return v;
+}
+
+// exp(x) for x <= 0 to about an fp32 ulp: 2^t with t = x log2 e rounded, times
+// the factor of what the rounding left (the hardware 2^t itself is within an
+// ulp).  Below -150, where the result is 0, x is cut off so that -inf stays
+// out of the remainder; NaN stays NaN.
+__device__ __forceinline__ float exp_neg(float x)
+{
+    x = x < -150.0f ? -150.0f : x;
+    constexpr float kHi = 1.44269502162933349609375f, kLo = 1.925963033500011e-8f;  // log2 e
+    const float t = x * kHi;
+    const float rest = fmaf(x, kLo, fmaf(x, kHi, -t));
+    const float e = __builtin_amdgcn_exp2f(t);
+    return fmaf(e, rest * 0.693147180559945f, e);
 }
 
 // Row of E logits -> exp(x - max) in x and the reciprocal of their sum.  A row
@@ -81,7 +128,7 @@ __device__ __forceinline__ float softmax_row(float (&x)[NV])
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        x[i] = expf(x[i] - m);
+        x[i] = exp_neg(x[i] - m);
         sum += x[i];
     }
     sum = wave_sum(sum);
@@ -104,11 +151,13 @@ template <int NV>
 __device__ __forceinline__ int balance_segment(const BalanceArgs &g, int a, int b,
                                                float (*red)[NV * kWave], int *hist, int *taken)
 {
-    constexpr int kTokens = NV >= 8 ? 1 : 2;  // rows of a wave in flight
+    constexpr int kTokens = NV >= 16 ? 1 : NV == 8 ? 2 : 4;  // rows of a wave in flight
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_id();
+    // the ids travel while the rows are worked on (T k <= 2^24)
+    const int i0 = a * g.k + tid, i1 = b * g.k;
+    const int id0 = i0 < i1 ? g.ids[i0] : -1;
     for (int e = tid; e < g.E; e += kBalanceThreads)
         hist[e] = 0;
-    __syncthreads();
 
     float sum[NV];
 #pragma unroll
@@ -133,17 +182,17 @@ __device__ __forceinline__ int balance_segment(const BalanceArgs &g, int a, int 
             n += in[q];
         }
     }
-    for (size_t i = (size_t)a * g.k + tid; i < (size_t)b * g.k; i += kBalanceThreads) {
-        const int e = g.ids[i];
-        if (e >= 0 && e < g.E && (!g.tok.mask || g.tok.mask[i / g.k]))
-            atomicAdd(&hist[e], 1);
-    }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         red[wave][lane + kWave * i] = sum[i];
     if (lane == 0)
         taken[wave] = n;
     __syncthreads();
+    for (int i = i0; i < i1; i += kBalanceThreads) {
+        const int e = i == i0 ? id0 : g.ids[i];
+        if (e >= 0 && e < g.E && (!g.tok.mask || g.tok.mask[i / g.k]))
+            atomicAdd(&hist[e], 1);
+    }
     for (int e = tid; e < g.E; e += kBalanceThreads) {
         float v = red[0][e];
 #pragma unroll
@@ -174,7 +223,7 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_chunk_kernel(BalanceA
     const int end = min((c + 1) * g.chunk, g.tok.T);
     int pos = max(c * g.chunk, seq_offset(g.tok, 0));
     while (pos < end) {
-        const int s = seq_behind(g.tok, pos);
+        const int s = seq_behind(g.tok, pos, tid & (kWave - 1));
         if (s >= g.tok.S)
             break;
         const int a = max(pos, seq_offset(g.tok, s)), b = min(end, seq_offset(g.tok, s + 1));
@@ -232,9 +281,7 @@ __global__ __launch_bounds__(kReduceRows * 64) void balance_reduce_kernel(Balanc
                 n += red_n[i][lane];
             }
         }
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1)
-            N += __shfl_xor(N, off);
+        N = wave_sum(N);
         const float inv = N > 0 ? 1.0f / (float)N : 0.0f;
         const float mean = p * inv;
         if (e < g.E) {
@@ -265,9 +312,7 @@ __global__ __launch_bounds__(kReduceRows * 64) void balance_reduce_kernel(Balanc
     for (int i = tid; i < g.tok.S; i += kReduceRows * 64)
         live += __hip_atomic_load(g.tokens + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) > 0;
     sum = wave_sum(sum);
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1)
-        live += __shfl_xor(live, off);
+    live = wave_sum(live);
     __syncthreads();
     if (lane == 0) {
         red_p[r][0] = sum;
@@ -328,30 +373,46 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_small_kernel(BalanceA
 // ------------------------------------------------------------ the gradient
 
 constexpr int kBackWaves = 4;
-constexpr int kRowFloats = 2048;  // LDS floats per wave for the scattered routing part
+constexpr int kRowFloats = 1024;  // LDS floats per wave for the scattered routing part
 
-// A wave takes a run of consecutive tokens, in batches of `batch` tokens whose
-// k slots its lanes hold side by side (kp lanes a token): one pass computes
-// their routing part and scatters it into rows in LDS; then each row is
+// Tokens of a batch: their slots fit the wave's lanes (kp = k rounded up to a
+// power of two), their rows its LDS and registers.
+constexpr int max_batch(int NV) { return NV >= 16 ? 1 : NV == 8 ? 2 : 4; }
+
+// A wave takes a run of consecutive tokens in batches of `batch`: the logits of
+// the whole batch are loaded first; then lanes side by side (kp a token)
+// compute the routing part and scatter it into rows in LDS; then each row is
 // finished and written.
 template <int NV, bool kSoftmax>
 __global__ __launch_bounds__(kBackWaves * kWave) void route_backward_kernel(RouteBackwardArgs g, int kp,
                                                                             int batch, int run)
 {
+    constexpr int kBatch = max_batch(NV);
     __shared__ float rows[kBackWaves][kRowFloats];
     __shared__ int live_part[kBackWaves];
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_id();
     float *row = rows[wave];
     const bool balance = g.counts != nullptr;
 
+    const long long first = ((long long)blockIdx.x * kBackWaves + wave) * run;
+    const int t_begin = (int)min((long long)g.tok.T, first), t_end = (int)min((long long)g.tok.T, first + run);
+    float x[kBatch][NV];
+    auto load_batch = [&](int t0) {
+        if (kSoftmax) {
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q)
+                if (q < batch)
+                    load_row(x[q], g.logits + (size_t)min(t0 + q, g.tok.T - 1) * g.E, g.E, lane);
+        }
+    };
+    load_batch(min(t_begin, g.tok.T - 1));
+
     float coef = 0.0f;
     if (balance) {  // dL E / (k S'), S' = sequences with tokens
         int live = 0;
         for (int i = tid; i < g.tok.S; i += kBackWaves * kWave)
             live += g.tokens[i] > 0;
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1)
-            live += __shfl_xor(live, off);
+        live = wave_sum(live);
         if (lane == 0)
             live_part[wave] = live;
         __syncthreads();
@@ -360,13 +421,12 @@ __global__ __launch_bounds__(kBackWaves * kWave) void route_backward_kernel(Rout
             live += live_part[w];
         coef = live > 0 ? *g.d_loss * (float)g.E / ((float)g.k * (float)live) : 0.0f;
     }
-
-    const long long first = ((long long)blockIdx.x * kBackWaves + wave) * run;
-    if (first >= g.tok.T)
+    if (t_begin >= t_end)
         return;
-    const int t_begin = (int)first, t_end = (int)min((long long)g.tok.T, first + run);
-    for (int i = lane; i < batch * g.E; i += kWave)
-        row[i] = 0.0f;
+    if (g.d_weights) {
+        for (int i = lane; i < batch * g.E; i += kWave)
+            row[i] = 0.0f;
+    }
 
     int seq = -1, seq_begin = 0, seq_end = 0;  // the sequence whose g is in registers
     float gr[NV];
@@ -377,13 +437,15 @@ __global__ __launch_bounds__(kBackWaves * kWave) void route_backward_kernel(Rout
     const int q_of = lane / kp, j_of = lane % kp;
     for (int t0 = t_begin; t0 < t_end; t0 += batch) {
         const int nb = min(batch, t_end - t0);
+        if (t0 > t_begin)
+            load_batch(t0);
         float inside = 0.0f;  // sum_i w_i dw_i of the lane's token
         int at = -1;
         if (g.d_weights) {
             const bool slot = q_of < nb && j_of < g.k;
-            const size_t x = (size_t)(t0 + (slot ? q_of : 0)) * g.k + (slot ? j_of : 0);
-            const int id = g.ids[x];
-            const float w = g.weights[x], dw = g.d_weights[x];
+            const size_t i = (size_t)(t0 + (slot ? q_of : 0)) * g.k + (slot ? j_of : 0);
+            const int id = g.ids[i];
+            const float w = g.weights[i], dw = g.d_weights[i];
             const bool ok = slot && id >= 0 && id < g.E;
             inside = ok ? w * dw : 0.0f;
             for (int off = kp >> 1; off >= 1; off >>= 1)
@@ -398,12 +460,12 @@ __global__ __launch_bounds__(kBackWaves * kWave) void route_backward_kernel(Rout
             if (__ballot(!alone)) {
                 float total = 0.0f;
                 bool is_first = true;
-                for (int i = 0; i < kp; ++i) {
-                    const int other = __shfl(at, q_of * kp + i);
-                    const float vi = __shfl(v, q_of * kp + i);
+                for (int o = 0; o < kp; ++o) {
+                    const int other = __shfl(at, q_of * kp + o);
+                    const float vo = __shfl(v, q_of * kp + o);
                     if (other == at) {
-                        total += vi;
-                        is_first = is_first && i >= j_of;
+                        total += vo;
+                        is_first = is_first && o >= j_of;
                     }
                 }
                 v = total;
@@ -414,10 +476,13 @@ __global__ __launch_bounds__(kBackWaves * kWave) void route_backward_kernel(Rout
             }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         }
-        for (int q = 0; q < nb; ++q) {
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            if (q >= nb)
+                break;
             const int t = t0 + q;
             if (t >= seq_end || t < seq_begin) {
-                seq = seq_behind(g.tok, t);
+                seq = seq_behind(g.tok, t, lane);
                 const bool real = seq < g.tok.S;
                 seq_begin = real ? seq_offset(g.tok, seq) : t;
                 seq_end = real ? seq_offset(g.tok, seq + 1) : g.tok.T;
@@ -445,18 +510,16 @@ __global__ __launch_bounds__(kBackWaves * kWave) void route_backward_kernel(Rout
                 d[i] = g.d_weights && e < g.E ? row[q * g.E + e] : 0.0f;
             }
             if (kSoftmax) {
-                float x[NV];
-                load_row(x, g.logits + (size_t)t * g.E, g.E, lane);
-                const float r = softmax_row(x);
+                const float r = softmax_row(x[q]);
                 float dot = 0.0f;
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
-                    dot += x[i] * gr[i];
+                    dot += x[q][i] * gr[i];
                 dot = wave_sum(dot) * r;
                 const float all = dot + (g.method == 1 ? __shfl(inside, q * kp) : 0.0f);
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
-                    d[i] += x[i] * r * (gr[i] - all);
+                    d[i] += x[q][i] * r * (gr[i] - all);
             }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -567,11 +630,10 @@ hipError_t launch_route_backward(const RouteBackwardArgs &a, hipStream_t s)
     int kp = 1;
     while (kp < a.k)
         kp *= 2;
-    // tokens whose slots fit the wave's lanes and whose rows fit its LDS
-    int batch = std::max(1, std::min(kWave / kp, kRowFloats / a.E));
+    const int nv = a.E <= 64 ? 1 : a.E <= 128 ? 2 : a.E <= 256 ? 4 : a.E <= 512 ? 8 : 16;
     // about 8 waves per SIMD when there are tokens for it
     const int per = (a.tok.T + 8191) / 8192;
-    batch = std::min(batch, per);
+    const int batch = std::max(1, std::min(std::min(kWave / kp, kRowFloats / a.E), std::min(max_batch(nv), per)));
     const int run = (per + batch - 1) / batch * batch;
     const int waves = (a.tok.T + run - 1) / run;
     const dim3 grid((waves + kBackWaves - 1) / kBackWaves), block(kBackWaves * kWave);
