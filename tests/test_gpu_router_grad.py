@@ -124,6 +124,43 @@ def test_route_backward(T, E, k, S, masked, head, tail, with_weights, with_balan
     assert (np.abs(got - want) <= rel * size).all()
 
 
+@pytest.mark.parametrize("T,E,k,S", [(70000, 5, 2, 65535), (300000, 16, 3, 7)])
+def test_many_sequences_and_tokens(T, E, k, S):
+    """As many sequences as there may be, a third of them empty, and long ones
+    over many chunks; bounds as above with the longest sequence's N."""
+    rng = np.random.default_rng(S)
+    mask, offsets = (rng.random(T) >= 0.1).astype(np.uint8), _offsets(rng, T, S, 3, 9)
+    x = rng.standard_normal((T, E)).astype(np.float32)
+    ids = np.argsort(-x, 1, kind="stable")[:, :k].astype(np.int32)
+    announce(f"balance_loss, route_backward T={T} S={S}")
+    sh = _shape(T, E, k)
+    r = binding.balance_loss(sh, _dev(x), _dev(ids), _dev(mask), _dev(offsets))
+    got = binding.route_backward(sh, _dev(x), balance=r, d_loss=torch.ones(1, device="cuda"),
+                                 token_mask=_dev(mask), seq_offsets=_dev(offsets)).cpu().numpy()
+    seq = np.searchsorted(offsets, np.arange(T), "right") - 1
+    seq = np.where((mask != 0) & (seq >= 0) & (seq < S), seq, -1)
+    live = seq >= 0
+    p = _router.softmax(x)
+    counts, total = np.zeros((S, E)), np.zeros((S, E))
+    tokens = np.bincount(seq[live], minlength=S)
+    np.add.at(counts, (np.repeat(seq[live], k), ids[live].reshape(-1)), 1)
+    np.add.at(total, seq[live], p[live])
+    inv = 1 / np.maximum(tokens, 1)[:, None]
+    probs = total * inv
+    loss = (E / k * inv * counts * probs).sum() / (tokens > 0).sum()
+    np.testing.assert_array_equal(r["counts"].cpu().numpy(), counts)
+    np.testing.assert_array_equal(r["tokens"].cpu().numpy(), tokens)
+    rel = (E + tokens.max() + 16 + 2 * (x.max() - x.min())) * F32
+    assert (np.abs(r["probs"].cpu().numpy() - probs) <= rel * probs).all()
+    assert abs(float(r["loss"]) - loss) <= (rel + (E + S + 8) * F32) * loss
+    g = E / k * inv ** 2 * counts / (tokens > 0).sum()
+    g = np.where(live[:, None], g[seq], 0)
+    inner = (p * g).sum(1, keepdims=True)
+    rel = (2 * E + 2 * k + 40 + 2 * (x.max() - x.min())) * F32
+    assert (np.abs(got - p * (g - inner)) <= rel * p * (g + inner)).all()
+    assert (got[~live] == 0).all()
+
+
 def test_empty_rows_and_extreme_logits():
     """Experts masked by -inf or by the type's lowest value, a row of -inf only
     (no distribution: probabilities and gradient 0), huge logits."""

@@ -65,6 +65,30 @@ def _draw(i):
                   int(rng.random() < 0.25), 700 + i)
 
 
+# Tiles of 64 rows (many slots) with experts that fill one to four row tiles,
+# K of several staged panels and an odd number of steps, the largest ranks and
+# adapter counts.
+LARGE = [
+    W4Case("tiles64", 4100, 128, 64, 3, 1, L=2, rg=16, rd=40),
+    W4Case("tiles64_few_rows_each", 1400, 320, 32, 100, 3, L=2, rg=8, rd=8, group=64),
+    W4Case("tiles64_zeros32", 2060, 192, 96, 24, 2, L=1, rg=8, rd=8, zeros=1, group=32),
+    W4Case("tiles64_rank256", 4100, 64, 64, 2, 1, L=2, rg=256, rd=256, zeros=1, group=64),
+    W4Case("tiles64_shared_odd_ranks", 2100, 128, 64, 8, 2, L=3, rg=13, rd=22, shared=1, group=32),
+    W4Case("tiles64_no_lora", 4200, 64, 32, 4, 1, zeros=1),
+    W4Case("tiles32_long_k", 400, 1216, 1088, 2, 1, L=1, rg=72, rd=8, group=64),
+    W4Case("tiles32_rank256", 300, 128, 64, 4, 2, L=2, rg=256, rd=200),
+    W4Case("panels_8_waves", 1, 4224, 1056, 4, 2, L=1, rg=40, rd=256, zeros=1, group=32),
+    W4Case("panels_4_waves", 60, 2240, 1120, 16, 2, L=2, rg=256, rd=36, group=64),
+    W4Case("adapters64", 200, 128, 64, 4, 2, L=64, rg=8, rd=8),
+    W4Case("adapters64_few_rows", 40, 128, 64, 8, 2, L=64, rg=36, rd=8, zeros=1, group=32),
+]
+
+
+@pytest.mark.parametrize("c", LARGE, ids=lambda c: c.name)
+def test_forward_w4_large(c):
+    test_forward_w4_matches_definition(c)
+
+
 @pytest.mark.parametrize("c", [_draw(i) for i in range(16)], ids=lambda c: c.name)
 def test_forward_w4_random_shapes(c):
     test_forward_w4_matches_definition(c)
