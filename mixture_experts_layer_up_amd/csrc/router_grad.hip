@@ -244,7 +244,7 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_chunk_kernel(BalanceA
 
 // Sums the chunks of one sequence for 64 experts; the block that finishes
 // last adds up the loss.
-constexpr int kReduceRows = 16;
+constexpr int kReduceRows = 8;
 
 __global__ __launch_bounds__(kReduceRows * 64) void balance_reduce_kernel(BalanceArgs g)
 {
@@ -295,14 +295,13 @@ __global__ __launch_bounds__(kReduceRows * 64) void balance_reduce_kernel(Balanc
                                __HIP_MEMORY_SCOPE_AGENT);
             if (blockIdx.x == 0)
                 __hip_atomic_store(g.tokens + s, N, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            __threadfence();
-            last = atomicAdd(g.ticket, 1u) == gridDim.x * gridDim.y - 1;
+            last = __hip_atomic_fetch_add(g.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+                   gridDim.x * gridDim.y - 1;
         }
     }
     __syncthreads();
     if (!last)
         return;
-    __threadfence();
     // every thread's share in ascending order, then a fixed tree
     float sum = 0.0f;
     int live = 0;
