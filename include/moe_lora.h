@@ -497,7 +497,8 @@ int moe_lora_balance_loss(const moe_lora_shape *shape, const float *router_logit
  *     moe_lora_balance_loss wrote them for the same `tokens` (loss and
  *     expert_probs are not read and may be NULL).  Counts are constants.
  * At least one part is given.  router_logits may be NULL when only the
- * routing weights' part of routing_method 0 is asked for.
+ * routing weights' part of routing_method 0 is asked for.  d_logits may be
+ * router_logits itself; it overlaps no other argument.
  */
 int moe_lora_route_backward(const moe_lora_shape *shape, const float *router_logits,
                             const int32_t *topk_ids, const float *topk_weights,
@@ -514,7 +515,8 @@ int moe_lora_route_backward(const moe_lora_shape *shape, const float *router_log
  *                  <d_out[t], expert_out[p]>, 0 for slots that are not local
  * One at least is given; d_expert_out needs topk_weights, d_topk_weights needs
  * expert_out.  bf16 pointers are 16-byte aligned.  A permuted index outside
- * [-1, T*k) counts as -1.
+ * [-1, T*k) counts as -1.  d_expert_out may be expert_out itself; outputs
+ * overlap no other argument.
  */
 int moe_lora_finalize_backward(const moe_lora_shape *shape, const void *d_out, const void *expert_out,
                                const int32_t *expanded_idx_to_permuted_idx, const float *topk_weights,

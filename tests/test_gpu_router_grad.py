@@ -294,6 +294,60 @@ def test_finalize_backward(T, H, k, local, scaling):
         assert abs(dw[t, j] - scaling * terms.sum()) <= scaling * (H + 4) * F32 * np.abs(terms).sum()
 
 
+def test_gradients_in_place():
+    """d_logits over router_logits and d_expert_out over expert_out: the same bits."""
+    T, E, k, H = 700, 96, 5, 320
+    rng = np.random.default_rng(21)
+    sh = _shape(T, E, k, 1, H)
+    x = _dev(rng.standard_normal((T, E)), np.float32)
+    ids = _dev(np.argsort(-x.cpu().numpy(), 1, kind="stable")[:, :k], np.int32)
+    w, dw = (_dev(rng.standard_normal((T, k)), np.float32) for _ in range(2))
+    one = torch.ones(1, device="cuda")
+    announce("in place")
+    bal = binding.balance_loss(sh, x, ids)
+    want = binding.route_backward(sh, x, ids, w, dw, balance=bal, d_loss=one)
+    here = x.clone()
+    binding.route_backward(sh, here, ids, w, dw, balance=bal, d_loss=one, d_logits=here)
+    assert torch.equal(here, want)
+    d, y = (_dev(rng.standard_normal((n, H)), np.float32).bfloat16() for n in (T, T * k))
+    r = {"expanded_idx_to_permuted_idx": _dev(rng.permutation(T * k), np.int32), "topk_weights": w}
+    dy, dw_want = binding.finalize_backward(sh, d, y, r)
+    _, dw_here = binding.finalize_backward(sh, d, y, r, d_expert_out=y)
+    assert torch.equal(y, dy) and torch.equal(dw_here, dw_want)
+
+
+def test_two_streams_at_once():
+    """Steps of different sizes on two streams, each with workspaces of its own."""
+    steps, want = [], []
+    for seed, T, E in ((1, 1500, 128), (2, 40, 64)):
+        c = _w4.W4Case("stream", T, 192, 96, E, 4, L=2, rg=8, rd=8, zeros=1, group=64, seed=seed)
+        x = _w4.inputs(c)
+        shape, fmt, hidden, packed, kw, logits = _w4.device_layer(c, x)
+        r = binding.alloc_routing(shape, "cuda")
+
+        def step(shape=shape, fmt=fmt, hidden=hidden, packed=packed, kw=kw, logits=logits, r=r):
+            out = binding.forward_w4(shape, fmt, hidden, *packed, router_logits=logits, routing=r, **kw)
+            bal = binding.balance_loss(shape, logits, r["topk_ids"])
+            d = binding.route_backward(shape, logits, balance=bal,
+                                       d_loss=torch.ones(1, device="cuda"))
+            return out, bal["loss"], d
+
+        steps.append(step)
+        want.append([t.clone() for t in step()])
+    announce("two streams")
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in steps]
+    got = [[], []]
+    for _ in range(8):
+        for i, (s, step) in enumerate(zip(streams, steps)):
+            with torch.cuda.stream(s):
+                got[i].append(step())
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        for run in runs:
+            assert all(torch.equal(a, b) for a, b in zip(run, w))
+
+
 def test_training_step_together():
     """forward_w4 with its expert outputs -> finalize -> balance loss -> the
     gradient of the router's logits, against the chain in float64."""
