@@ -405,9 +405,7 @@ int enqueue_gemm_w4(const GemmArgs &g, const moe_lora_w4_format *w4, bool gated,
     const uint8_t *packed = reinterpret_cast<const uint8_t *>(g.Wp);
     GemmW4Args a{};
     a.X = g.X;
-    a.gather_by_token = g.gather_by_token;
     a.K = g.K;
-    a.N = g.n_canon;
     a.codes = packed;
     a.scales = reinterpret_cast<const uint16_t *>(packed + l.scales);
     a.zeros = w4->zero_points ? packed + l.zeros : nullptr;

@@ -28,7 +28,7 @@
 namespace moe_lora {
 namespace {
 
-constexpr int kMinBlocks = 1024;  // two rounds of two blocks per CU
+constexpr int kMinBlocks = 1024;  // two rounds of two blocks per CU (700 to 4096: the same times; 400: +38%)
 
 // A block's share: what the whole block agrees on.
 struct Job {

@@ -28,9 +28,8 @@ struct PackW4Args {
 
 // Grouped expert product with 4-bit weights, the LoRA expand folded in.
 struct GemmW4Args {
-    const uint16_t *X;        // gather_by_token ? hidden [T, K] : act [n, K]
-    int gather_by_token;
-    int K, N;
+    const uint16_t *X;        // gate_up: hidden [T, K]; down: act [n, K]
+    int K;
     const uint8_t *codes;     // the packed weight's regions (w4_layout.h)
     const uint16_t *scales;
     const uint8_t *zeros;     // or null

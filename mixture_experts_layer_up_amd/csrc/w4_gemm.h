@@ -35,7 +35,7 @@ typedef u32x4 __attribute__((aligned(2))) u32x4_unaligned;
 constexpr int kStepChunks = 4;  // 32-row chunks of a step
 constexpr int kStepBytes = 2 * kW4UnitBytes;
 
-// The constants of decode_w4, opaque to the compiler and in the two kinds of
+// Decoding.  Its constants are opaque to the compiler and in the two kinds of
 // register one v_and_or_b32 can take (as literals it would split each into an
 // and and an or).
 struct DecodeW4 {
