@@ -221,7 +221,11 @@ typedef struct moe_lora_routing {
  *                      gate_up GEMM.  Nothing is allocated, so a two-stream
  *                      forward can be captured into a HIP graph.  Not
  *                      touched when side_stream is ignored (see above).
- * LoRA pointers may be NULL when the projection is inactive.
+ * LoRA pointers may be NULL when the projection is inactive.  The values of
+ * lora_b_gate_up and lora_b_down must be finite: a row meets the expand weights
+ * of the adapters it does not use as factors of zero, so an infinity or NaN in
+ * one adapter's stack can make the output of any token NaN (not so in
+ * moe_lora_forward_w4).
  */
 typedef struct moe_lora_inputs {
     const void *hidden;
@@ -427,7 +431,9 @@ int moe_lora_pack_weights_w4(const moe_lora_shape *shape, const moe_lora_w4_form
  * activations and the output.  Without expert_out the slots' expert outputs
  * stay fp32 until the routing-weighted sum, so `out` and a moe_lora_finalize of
  * the (bf16) expert_out agree to the rounding of expert_out, not bitwise.  A
- * token whose hidden row holds an infinity or NaN gets non-finite outputs.
+ * token whose hidden row holds an infinity or NaN gets non-finite outputs (if it
+ * has a local slot); one in an adapter's stacks makes outputs of that adapter's
+ * tokens non-finite.  Neither reaches another token.
  */
 size_t moe_lora_workspace_size_w4(const moe_lora_shape *shape, const moe_lora_w4_format *format);
 

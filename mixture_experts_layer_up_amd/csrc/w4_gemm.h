@@ -300,8 +300,30 @@ __device__ __forceinline__ ExpandStep next_expand(ExpandStep e, unsigned long lo
     return ExpandStep{l, 0};
 }
 
+// Whether an expand step's operand may hold an infinity or NaN.  Read as fp16,
+// those bf16 bit patterns are all NaN, and so are the finite ones above 2^121,
+// which only cost time; a NaN survives a maximum.
+__device__ __forceinline__ bool maybe_nonfinite(const u32x4 (&b)[kNS])
+{
+    typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
+    f16x2 top = {0, 0};
+#pragma unroll
+    for (int n = 0; n < kNS; ++n) {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const uint32_t u = b[n][i], v = b[n][i + 1];
+            top = __builtin_elementwise_maximum(
+                __builtin_elementwise_maximum(top, __builtin_bit_cast(f16x2, u)), __builtin_bit_cast(f16x2, v));
+        }
+    }
+    return top.x != top.x || top.y != top.y;
+}
+
 // The whole expand of a wave, over NM of MT row tiles, with NE steps' operands
 // in flight: the steps of `used` adapters in order, each its rank positions.
+// Rows of other adapters, or of none, meet an adapter's B rows as zeros.  Where
+// a B row holds an infinity or NaN, 0 times it is NaN, so steps that may
+// hold one are left for a second pass, which adds to the adapter's own rows only.
 template <int NM, int MT, int NE>
 struct Expand {
     unsigned long long used;
@@ -330,6 +352,7 @@ struct Expand {
     __device__ __forceinline__ void run(f32x4 (&acc)[NM][kNS], const GemmW4Args &a, const SlabW4 &w, int I,
                                         uint32_t adapters, const u32x4 *sfrag, int lane)
     {
+        unsigned long long wild = 0;  // adapters with steps left for run_wild
         while (e[0].l >= 0) {
 #pragma unroll
             for (int i = 0; i < NE; ++i) {
@@ -337,15 +360,51 @@ struct Expand {
                     continue;
                 if (a.r & 7)
                     fix_expand(b[i], a, w, e[i], I, lane);
+                if (__ballot(maybe_nonfinite(b[i]))) {  // uniform
+                    wild |= 1ull << e[i].l;
+                } else {
 #pragma unroll
-                for (int m = 0; m < NM; ++m) {
-                    const u32x4 v = keep_if(sfrag[(e[i].q0 / 32 * MT + m) * kWave + lane],
-                                            ((adapters >> (8 * m)) & 0xffu) == (uint32_t)e[i].l);
+                    for (int m = 0; m < NM; ++m) {
+                        const u32x4 v = keep_if(sfrag[(e[i].q0 / 32 * MT + m) * kWave + lane],
+                                                ((adapters >> (8 * m)) & 0xffu) == (uint32_t)e[i].l);
 #pragma unroll
-                    for (int n = 0; n < kNS; ++n)
-                        acc[m][n] = mfma_16x16x32(v, b[i][n], acc[m][n]);
+                        for (int n = 0; n < kNS; ++n)
+                            acc[m][n] = mfma_16x16x32(v, b[i][n], acc[m][n]);
+                    }
                 }
                 load(i, a, w, I, lane);
+            }
+        }
+        if (wild)
+            run_wild(acc, wild, a, w, I, adapters, sfrag, lane);
+    }
+    // The steps that may hold infinities or NaN of the adapters in `wild`: products apart
+    // from the sums, added to the rows of the step's adapter only.
+    __device__ __forceinline__ void run_wild(f32x4 (&acc)[NM][kNS], unsigned long long wild, const GemmW4Args &a,
+                                             const SlabW4 &w, int I, uint32_t adapters, const u32x4 *sfrag,
+                                             int lane)
+    {
+        for (ExpandStep s = next_expand(ExpandStep{-1, 0}, &wild, a.r); s.l >= 0; s = next_expand(s, &wild, a.r)) {
+            u32x4 v[kNS];
+            load_expand(v, a, w, s, I, lane);
+            if (a.r & 7)
+                fix_expand(v, a, w, s, I, lane);
+            if (!__ballot(maybe_nonfinite(v)))
+                continue;
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                const u32x4 x = sfrag[(s.q0 / 32 * MT + m) * kWave + lane];
+                unsigned own = 0;  // bit j: row 4 (lane / 16) + j is the adapter's
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    own |= (((__shfl(adapters, (lane >> 4) * 4 + j) >> (8 * m)) & 0xffu) == (uint32_t)s.l) << j;
+#pragma unroll
+                for (int n = 0; n < kNS; ++n) {
+                    const f32x4 part = mfma_16x16x32(x, v[n], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        acc[m][n][j] += (own >> j) & 1 ? part[j] : 0.0f;
+                }
             }
         }
     }
