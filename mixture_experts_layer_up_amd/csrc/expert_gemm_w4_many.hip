@@ -24,11 +24,10 @@
 #include <algorithm>
 
 #include "w4_gemm.h"
+#include "w4_launch.h"
 
 namespace moe_lora {
 namespace {
-
-constexpr int kMinBlocks = 1024;  // two rounds of two blocks per CU (700 to 4096: the same times; 400: +38%)
 
 // A block's share: what the whole block agrees on.
 struct Job {
@@ -175,11 +174,8 @@ template <int MT, int G, bool kGated, bool kZeros>
 hipError_t launch_many(const GemmW4Args &a, hipStream_t s)
 {
     const int n_sg = (a.n_slabs + 3) / 4;
-    // slab groups per block: as many as still leave that many blocks
     const int tiles = std::min(a.n_tiles, std::max(a.n_busy, a.n_slots / a.tile_rows));
-    int per = 1;
-    while (per < n_sg && (long long)tiles * ((n_sg + per) / (per + 1)) >= kMinBlocks)
-        ++per;
+    const int per = w4_groups_per_block(tiles, n_sg);
     const int blocks = (a.n_tiles * ((n_sg + per - 1) / per) + 7) / 8 * 8;
     const int lds = 2 * (4 / MT) * step_lds_bytes(MT, G) + (a.S ? (a.r + 31) / 32 * MT * 1024 : 0);
     hipLaunchKernelGGL((expert_gemm_w4_many_kernel<MT, G, kGated, kZeros>), dim3(blocks), dim3(256), lds, s, a,
