@@ -20,6 +20,21 @@ int main()
 }
 """
 
+# Layers (arguments of a case in _w4.py) whose products run several slab groups
+# a block; what each product's column count gives is asserted below and their
+# results in test_gpu_w4_blocks.py.  32- and 64-row tiles; K of one, an even and an
+# odd number of steps; a shorter last job; column counts that end inside a group;
+# adapters.
+BLOCKS = [
+    dict(name="rows32_down", T=4000, H=4288, I=96, E=4, k=1, L=2, rg=8, rd=16, group=32, zeros=1),
+    dict(name="rows32_down_whole_jobs", T=4000, H=4608, I=128, E=4, k=1, L=2, rg=0, rd=40, group=128),
+    dict(name="rows32_gate_up", T=4000, H=320, I=2144, E=4, k=1, L=2, rg=13, rd=8, group=64, zeros=1),
+    dict(name="rows32_gate_up_even", T=4000, H=192, I=2208, E=4, k=1, L=3, rg=40, rd=0, group=128),
+    dict(name="rows64_down", T=8200, H=4288, I=64, E=3, k=1, L=2, rg=8, rd=72, group=64, zeros=1),
+    dict(name="rows64_both", T=16400, H=1280, I=608, E=4, k=2, L=2, rg=16, rd=8, group=128),
+    dict(name="rows64_gate_up", T=8200, H=320, I=2144, E=3, k=1, L=2, rg=64, rd=8, group=32, zeros=1),
+]
+
 
 @pytest.fixture(scope="session")
 def rule(tmp_path_factory):
@@ -48,3 +63,15 @@ def test_groups_per_block_are_even_and_make_enough_blocks(rule):
         # one job fewer, where the groups can be cut so
         fewer = [j for j in range(1, jobs) if -(-n_sg // -(-n_sg // j)) == j]
         assert not fewer or tiles * fewer[-1] < 1024
+
+
+@pytest.mark.parametrize("c", BLOCKS, ids=lambda c: c["name"])
+def test_blocks_cases_run_several_groups(rule, c):
+    rows = int(c["name"][4:6])
+    tiles = c["T"] * c["k"] // rows
+    n_sg = {"gate_up": -(-2 * c["I"] // 256), "down": -(-c["H"] // 256)}
+    named = [p for p in n_sg if p in c["name"]] or list(n_sg)
+    per = dict(zip(named, rule([(tiles, n_sg[p]) for p in named])))
+    assert all(2 <= v <= n_sg[p] for p, v in per.items()), per
+    short = {p for p, v in per.items() if n_sg[p] % v}
+    assert bool(short) == (c["name"] not in ("rows32_down_whole_jobs", "rows32_gate_up_even"))
