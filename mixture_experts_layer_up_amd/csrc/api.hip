@@ -21,6 +21,7 @@
 #include "kernels_router.h"
 #include "kernels_w4.h"
 #include "moe_lora.h"
+#include "w4_launch.h"
 #include "w4_layout.h"
 
 using namespace moe_lora;
@@ -116,7 +117,7 @@ Layout make_layout(const moe_lora_shape *s, const moe_lora_w4_format *w4 = nullp
     L.seg_offsets = take((segs + 1) * 4);
     L.seg_slots = take(n * 4);
     L.perm_scratch = take(permute_scratch_bytes((int)n, (int)el, s->num_loras));
-    L.tile_rows = w4 ? gemm_w4_tile_rows((int)n, s->num_experts, (int)el)
+    L.tile_rows = w4 ? w4_tile_rows((int)n, s->num_experts, (int)el)
                      : gemm_tile_rows((int)n, (int)el, s->hidden, s->inter,
                                       lora_gate_up_active(s) ? s->rank_gate_up : 0,
                                       lora_down_active(s) ? s->rank_down : 0);
@@ -399,7 +400,7 @@ int validate_inputs(const moe_lora_shape *shape, const moe_lora_inputs *in,
 // One of the two expert products with 4-bit weights, from the bf16 product's
 // argument block (same rows, work list and LoRA operands).
 int enqueue_gemm_w4(const GemmArgs &g, const moe_lora_w4_format *w4, bool gated, void *y, bool y_f32,
-                    int n_slots, hipStream_t st)
+                    int n_local, hipStream_t st)
 {
     const W4Layout l = w4_layout(g.E_l, g.K, g.n_canon, w4->group, w4->zero_points != 0);
     const uint8_t *packed = reinterpret_cast<const uint8_t *>(g.Wp);
@@ -426,8 +427,8 @@ int enqueue_gemm_w4(const GemmArgs &g, const moe_lora_w4_format *w4, bool gated,
     a.tile_count = g.tile_count;
     a.n_tiles = g.n_tiles;
     a.tile_rows = g.tile_rows;
-    a.n_slots = n_slots;
-    a.n_busy = n_slots < g.E_l ? n_slots : g.E_l;
+    a.n_local = n_local;
+    a.n_busy = n_local < g.E_l ? n_local : g.E_l;
     a.perm2exp = g.perm2exp;
     a.E_l = g.E_l;
     a.k = g.k;
@@ -561,6 +562,7 @@ int forward_impl(const moe_lora_shape *shape, const moe_lora_inputs *in,
         MOE_TRY(check(launch_shrink(sa_gu, st)));
     MOE_TRY(record(ev, 2, st));
 
+    const int n_local = w4_local_slots(T * k, shape->num_experts, E_l);
     GemmArgs g1{};
     g1.X = hidden;
     g1.gather_by_token = 1;
@@ -589,7 +591,7 @@ int forward_impl(const moe_lora_shape *shape, const moe_lora_inputs *in,
     };
     g1.n_slabs = slabs(g1.NT);
     g1.zeros = static_cast<const uint16_t *>(zeros);
-    MOE_TRY(w4 ? enqueue_gemm_w4(g1, w4, true, act, false, T * k, st) : check(launch_gemm_gate_up(g1, st)));
+    MOE_TRY(w4 ? enqueue_gemm_w4(g1, w4, true, act, false, n_local, st) : check(launch_gemm_gate_up(g1, st)));
     MOE_TRY(record(ev, 3, st));
 
     if (dn) {
@@ -626,7 +628,7 @@ int forward_impl(const moe_lora_shape *shape, const moe_lora_inputs *in,
     g2.zeros = static_cast<const uint16_t *>(zeros);
     g2.lb_shared = shape->lora_shared_outer;
     const bool y_f32 = w4 && !expert_out;
-    MOE_TRY(w4 ? enqueue_gemm_w4(g2, w4, false, y, y_f32, T * k, st) : check(launch_gemm_down(g2, st)));
+    MOE_TRY(w4 ? enqueue_gemm_w4(g2, w4, false, y, y_f32, n_local, st) : check(launch_gemm_down(g2, st)));
     MOE_TRY(record(ev, 5, st));
 
     if (y_f32) {

@@ -19,6 +19,7 @@
 #include <algorithm>
 
 #include "w4_gemm.h"
+#include "w4_launch.h"
 
 namespace moe_lora {
 namespace {
@@ -145,17 +146,6 @@ __global__ __launch_bounds__(NW * kWave, 3) void expert_gemm_w4_kernel(GemmW4Arg
         store_slab<1, kGated>(acc, a, row0, n_rows, w.slab, lane);
 }
 
-// Shares of K per slab: 1 when the slabs alone make a wave per SIMD,
-// doubling until they do or a share has no step left.
-int k_shares_log(const GemmW4Args &a)
-{
-    const long long slabs = (long long)std::min(a.n_tiles, a.n_busy) * a.n_slabs;
-    int log = 0;
-    while (log < 3 && (slabs << log) < 1024 && (a.k_units / 2 >> (log + 1)) >= 1)
-        ++log;
-    return log;
-}
-
 template <int NW, int G, bool kGated, bool kZeros>
 hipError_t launch_few(const GemmW4Args &a, int log, hipStream_t s)
 {
@@ -171,22 +161,6 @@ hipError_t launch_few(const GemmW4Args &a, int log, hipStream_t s)
 
 } // namespace
 
-int gemm_w4_tile_rows(int n_slots, int E, int E_l)
-{
-    // Rows an expert gets on average, and slots this shard gets, when the
-    // routing is uniform.  Layer times in us with 16 / 32 / 64 rows a tile, on
-    // 128 experts top-8 (hidden 2048, inter 768): 12 rows 117 / 123 / 132, 20
-    // rows 150 / 131 / 138, 32 rows 180 / 174 / 152; with fewer experts 32 rows
-    // a tile stay ahead until there are blocks enough for 64: 32 local
-    // experts, 64 rows each, 142 / 111 / 124, 128 rows 220 / 276 / 150; and 16
-    // while a batch is a handful of tiles: 8 experts, 32 rows, 34 / 41 / 45.
-    const int mean = n_slots / E;
-    const long long local = (long long)n_slots * E_l / E;
-    if (mean <= 16 || local <= 320)
-        return 16;
-    return mean >= 24 && local >= 4096 ? 64 : 32;
-}
-
 hipError_t launch_gemm_w4(const GemmW4Args &a, bool gated, hipStream_t s)
 {
     if (a.n_tiles <= 0)
@@ -194,7 +168,7 @@ hipError_t launch_gemm_w4(const GemmW4Args &a, bool gated, hipStream_t s)
     if (a.tile_rows > 16)
         return launch_gemm_w4_many(a, gated, s);
     return with_format(a.group, gated, a.zeros != nullptr, [&](auto G, auto gt, auto zr) {
-        const int log = k_shares_log(a);
+        const int log = w4_k_shares_log(std::min(a.n_tiles, a.n_busy), a.n_slabs, a.k_units / 2);
         return log == 3 ? launch_few<8, G(), gt(), zr()>(a, log, s) : launch_few<4, G(), gt(), zr()>(a, log, s);
     });
 }

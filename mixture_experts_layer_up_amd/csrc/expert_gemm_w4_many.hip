@@ -21,8 +21,6 @@
 // 1000 and 700 cycles, and two waves per SIMD overlap them only in part.  The
 // LoRA expand is 35 and 53 us of it: every 64-row tile loads its slab's B rows
 // (half a cache line a row and step) again.
-#include <algorithm>
-
 #include "w4_gemm.h"
 #include "w4_launch.h"
 
@@ -174,8 +172,7 @@ template <int MT, int G, bool kGated, bool kZeros>
 hipError_t launch_many(const GemmW4Args &a, hipStream_t s)
 {
     const int n_sg = (a.n_slabs + 3) / 4;
-    const int tiles = std::min(a.n_tiles, std::max(a.n_busy, a.n_slots / a.tile_rows));
-    const int per = w4_groups_per_block(tiles, n_sg);
+    const int per = w4_groups_per_block(w4_row_tiles(a.n_tiles, a.n_busy, a.n_local, a.tile_rows), n_sg);
     const int blocks = (a.n_tiles * ((n_sg + per - 1) / per) + 7) / 8 * 8;
     const int lds = 2 * (4 / MT) * step_lds_bytes(MT, G) + (a.S ? (a.r + 31) / 32 * MT * 1024 : 0);
     hipLaunchKernelGGL((expert_gemm_w4_many_kernel<MT, G, kGated, kZeros>), dim3(blocks), dim3(256), lds, s, a,

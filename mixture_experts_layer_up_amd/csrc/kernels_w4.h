@@ -43,7 +43,7 @@ struct GemmW4Args {
     const int4 *tiles;        // work list written by the permute kernel
     const int32_t *tile_count;
     int n_tiles, tile_rows;   // list length (upper bound), rows per tile
-    int n_slots, n_busy;      // slots n, and experts they can touch: min(n, E_l)
+    int n_local, n_busy;      // slots of this shard on average, and experts they can touch
     const int32_t *perm2exp;  // [n]
     int E_l, k, I;
     void *Y;                  // gate_up: bf16 act [n, I]; down: [n, n_canon]
@@ -59,8 +59,6 @@ struct FinalizeF32Args {
     float scale;
 };
 
-// Rows per work-list tile (16, 32 or 64) for n slots over E experts, E_l of them local.
-int gemm_w4_tile_rows(int n_slots, int E, int E_l);
 hipError_t launch_gemm_w4(const GemmW4Args &a, bool gated, hipStream_t s);
 hipError_t launch_gemm_w4_many(const GemmW4Args &a, bool gated, hipStream_t s);  // tiles of 32, 64 rows
 hipError_t launch_finalize_f32(const FinalizeF32Args &a, hipStream_t s);
