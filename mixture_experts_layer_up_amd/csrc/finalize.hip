@@ -69,8 +69,18 @@ hipError_t launch_finalize(const FinalizeArgs &a, hipStream_t s)
     if (a.T <= 0)
         return hipSuccess;
     const int col_blocks = (a.H + 2047) / 2048;
-    hipLaunchKernelGGL(finalize_kernel, dim3(a.T, col_blocks), dim3(256), 0, s, a);
-    return hipGetLastError();
+    constexpr int kMaxTokens = 1 << 23;  // a launch may have 2^32 - 1 threads in x
+    for (int t0 = 0; t0 < a.T; t0 += kMaxTokens) {
+        FinalizeArgs b = a;
+        b.exp2perm += (size_t)t0 * a.k;
+        b.weights += (size_t)t0 * a.k;
+        b.out += (size_t)t0 * a.H;
+        hipLaunchKernelGGL(finalize_kernel, dim3(min(kMaxTokens, a.T - t0), col_blocks), dim3(256), 0, s, b);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 } // namespace moe_lora

@@ -58,8 +58,18 @@ hipError_t launch_finalize_f32(const FinalizeF32Args &a, hipStream_t s)
     if (a.T <= 0)
         return hipSuccess;
     const int col_blocks = (a.H + 1023) / 1024;
-    hipLaunchKernelGGL(finalize_f32_kernel, dim3(a.T, col_blocks), dim3(256), 0, s, a);
-    return hipGetLastError();
+    constexpr int kMaxTokens = 1 << 23;  // a launch may have 2^32 - 1 threads in x
+    for (int t0 = 0; t0 < a.T; t0 += kMaxTokens) {
+        FinalizeF32Args b = a;
+        b.exp2perm += (size_t)t0 * a.k;
+        b.weights += (size_t)t0 * a.k;
+        b.out += (size_t)t0 * a.H;
+        hipLaunchKernelGGL(finalize_f32_kernel, dim3(min(kMaxTokens, a.T - t0), col_blocks), dim3(256), 0, s, b);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 } // namespace moe_lora
