@@ -592,7 +592,8 @@ def route_backward(shape: Shape, router_logits: Optional[torch.Tensor],
                    d_logits: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of the router logits, fp32 [T, E]: the part of the routing weights
     (``d_topk_weights`` fp32 [T, k]) plus that of the balance loss (``balance`` as
-    :func:`balance_loss` returned it for the same tokens, ``d_loss`` fp32 [1]).
+    :func:`balance_loss` returned it for the same tokens, ``d_loss`` fp32 [1] or
+    without dimensions).
     Rows of tokens that take no part are 0."""
     T, E, k = shape.num_tokens, shape.num_experts, shape.top_k
     if (balance is None) != (d_loss is None):
@@ -612,7 +613,7 @@ def route_backward(shape: Shape, router_logits: Optional[torch.Tensor],
             _ptr(topk_ids, torch.int32, (T, k), "topk_ids"),
             _ptr(topk_weights, torch.float32, (T, k), "topk_weights"),
             _ptr(d_topk_weights, torch.float32, (T, k), "d_topk_weights"), tokens, bal,
-            _ptr(d_loss, torch.float32, (1,), "d_loss"),
+            _ptr(d_loss, torch.float32, () if d_loss is not None and d_loss.dim() == 0 else (1,), "d_loss"),
             _ptr(d_logits, torch.float32, (T, E), "d_logits"))
     _check(_on(gpu, lambda stream: load_library().moe_lora_route_backward(*args, stream)))
     return d_logits
