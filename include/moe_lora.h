@@ -427,13 +427,16 @@ int moe_lora_pack_weights_w4(const moe_lora_shape *shape, const moe_lora_w4_form
  * `format`, and a workspace of moe_lora_workspace_size_w4 bytes.  Everything
  * else (routing, bf16 LoRA stacks, expert parallelism, the side stream, events,
  * expert_out, the empty batch) is as there.  The weights enter the products
- * exactly; sums are fp32.  Rounded to bf16 are the LoRA shrink outputs, the
- * activations and the output.  Without expert_out the slots' expert outputs
- * stay fp32 until the routing-weighted sum, so `out` and a moe_lora_finalize of
- * the (bf16) expert_out agree to the rounding of expert_out, not bitwise.  A
- * token whose hidden row holds an infinity or NaN gets non-finite outputs (if it
- * has a local slot); one in an adapter's stacks makes outputs of that adapter's
- * tokens non-finite.  Neither reaches another token.
+ * exactly; sums are fp32, of terms x (16 + code) and x (16 + zero point), so
+ * their error is relative to sum |x| scale, also where weights are 0, and finite
+ * activations above about 8e34 may overflow.  Rounded to bf16 are the LoRA
+ * shrink outputs, the activations and the output.  Without expert_out the slots'
+ * expert outputs stay fp32 until the routing-weighted sum, so `out` and a
+ * moe_lora_finalize of the (bf16) expert_out agree to the rounding of
+ * expert_out, not bitwise.  A token whose hidden row holds an infinity or NaN
+ * gets non-finite outputs (if it has a local slot); one in an adapter's stacks
+ * makes outputs of that adapter's tokens non-finite.  Neither reaches another
+ * token.
  */
 size_t moe_lora_workspace_size_w4(const moe_lora_shape *shape, const moe_lora_w4_format *format);
 

@@ -10,9 +10,12 @@
 // and per group, with x's group sum xs taken by MFMAs against ones when the
 // activations are staged (once for all columns),
 //   sum_k x_k w_k = s ( sum_k x_k (16 + q_k)  -  (16 + z) sum_k x_k )
-// in fp32.  bf16 products are exact in fp32, so the only roundings are the
-// fp32 sums'; the subtraction cancels at most a factor of about (16 + z) / 8
-// of their 24 bits.
+// in fp32.  bf16 products are exact in fp32, so the only roundings are the fp32
+// sums', of terms of size (16 + q) |x| and (16 + z) |x|.  The error of a column
+// is thus at most about (K + group) 2^-24 sum_k s (32 + q_k + z) |x_k|, absolute:
+// where the sum itself cancels (a weight of 0, activations of one sign), it does
+// not shrink with it.  For the same reason a group sum overflows when 31 times
+// the sum of its |x| does, that is for activations above about 8e34.
 //
 // A wave's work is one 64-column slab: K in steps of 128 rows, and the LoRA
 // expand as more K: per adapter that the tile's rows use, steps of 32 rank
