@@ -554,8 +554,24 @@ void with_nv(int E, F f)
         f(std::integral_constant<int, 16>{});
 }
 
-// Batches that one block does: up to 128 tokens and 16 sequences.
-bool balance_is_small(int T, int S) { return T <= 128 && S <= 16; }
+// Batches that one block does: where its walk through the sequences, one after
+// another, is shorter than a second launch.  One block / two launches in us, by
+// sequences:       1           2           4           8          16
+//   32 tokens, 128 experts
+//              3.9 / 8.5   6.0 / 10.7  10.5 / 15.4  16.9 / 21.8  32.3 / 37.0
+//   64 tokens, 128 experts
+//              5.1 / 8.5   6.2 / 8.2   10.6 / 10.8  19.8 / 15.5  32.3 / 21.9
+//   64 tokens, 256 experts
+//              6.1 / 9.1   7.3 / 9.2   12.8 / 12.1  24.3 / 17.9  38.1 / 24.8
+//   128 tokens, 128 experts
+//              8.0 / 8.3   8.7 / 8.6   10.8 / 8.6   19.9 / 11.1  38.0 / 15.7
+//   128 tokens, 256 experts
+//             10.1 / 8.9  10.6 / 9.2   13.1 / 9.3   24.3 / 12.1  47.1 / 18.2
+// 32 tokens are one chunk of the two launches, which walk them as well.
+bool balance_is_small(int T, int E, int S)
+{
+    return T <= 32 ? S <= 16 : T <= 128 && T * E <= 16384 && T * S <= 256;
+}
 
 } // namespace
 
@@ -591,7 +607,7 @@ BalanceLayout balance_regions(int T, int E, int S)
 
 size_t balance_workspace(int T, int E, int S)
 {
-    return balance_is_small(T, S) ? 0 : balance_regions(T, E, S).total;
+    return balance_is_small(T, E, S) ? 0 : balance_regions(T, E, S).total;
 }
 
 void balance_layout(BalanceArgs *a, void *workspace)
@@ -609,7 +625,7 @@ void balance_layout(BalanceArgs *a, void *workspace)
 
 hipError_t launch_balance(const BalanceArgs &a, hipStream_t s)
 {
-    if (balance_is_small(a.tok.T, a.tok.S)) {
+    if (balance_is_small(a.tok.T, a.E, a.tok.S)) {
         with_nv(a.E, [&](auto nv) {
             hipLaunchKernelGGL((balance_small_kernel<decltype(nv)::value>), dim3(1),
                                dim3(kBalanceThreads), 0, s, a);
