@@ -456,7 +456,9 @@ int moe_lora_forward_w4(const moe_lora_shape *shape, const moe_lora_w4_format *f
  *                 unspecified values but no access outside the arrays.
  *   num_sequences S, 1 .. 65535
  * Logits, ids, weights and gradients of padding tokens are never used, so they
- * may hold anything.
+ * may hold anything.  Padding is padding for everything a call computes: to leave
+ * tokens out of the balance loss but not out of the routing weights' gradient,
+ * call moe_lora_route_backward for each part and add the two.
  */
 typedef struct moe_lora_tokens {
     const uint8_t *token_mask;

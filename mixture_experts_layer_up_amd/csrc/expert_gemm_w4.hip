@@ -13,9 +13,11 @@
 // Measured with hidden 2048, inter 768, 128 experts top-8, rank-16 adapters:
 // 64 tokens (group 64, zero points) gate_up 40 us for 231 MB from HBM, 5.7
 // TB/s (a large copy on the same card: 4.9), down 29 us for 127 MB.  A ring of
-// three steps, or four waves per SIMD, spill registers and are slower.  One
-// token 8.2 and 6.3 us: latency, the work list, its rows, the activations and
-// the first codes being loaded in turn.
+// three steps, or four waves per SIMD, spill registers and are slower.  Groups of
+// 32 with zero points spill 2 and 4 registers as it is, stored once and loaded
+// once a panel: 64 tokens 108 us a layer, 101 without zero points, 96 in groups
+// of 128.  One token 8.4 and 6.8 us: latency, the work list, its rows, the
+// activations and the first codes being loaded in turn.
 #include <algorithm>
 
 #include "w4_gemm.h"

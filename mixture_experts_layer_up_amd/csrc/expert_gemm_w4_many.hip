@@ -14,13 +14,20 @@
 //
 // Measured with hidden 2048, inter 768, 128 experts top-8: 384 tokens, rank 16,
 // gate_up 60 us and down 48 us for 233 and 137 MB of weights and adapters: 3.9
-// and 2.9 TB/s, between the stream's rate and the loop's issue.  2048 tokens, rank 64: gate_up 171..204 us
-// (machines differ in clock), down 144..163 us, with the matrix units busy 30%
-// and 21% of the time.  What bounds that is a wave's own issue: per step and
-// wave the MFMAs, the LDS reads and the decoding and scaling take about 1000,
-// 1000 and 700 cycles, and two waves per SIMD overlap them only in part.  The
-// LoRA expand is 35 and 53 us of it: every 64-row tile loads its slab's B rows
-// (half a cache line a row and step) again.
+// and 2.9 TB/s, between the stream's rate and the loop's issue.  2048 tokens,
+// rank 64: gate_up 171..204 us (machines differ in clock), down 144..163 us, with
+// the matrix units busy 30% and 21% of the time.  What bounds that is a wave's
+// own issue: per step and wave the MFMAs, the LDS reads and the decoding and
+// scaling take about 1000, 1000 and 700 cycles, and two waves per SIMD overlap
+// them only in part.  The LoRA expand is 17 and 52 us of it (181 and 153 us against 164 and 101 without
+// adapters): every 64-row tile loads its slab's B rows (half a cache line a row
+// and step) again.
+//
+// Groups of 32 rows hold four groups' scales and zero points per step: with zero
+// points or 64-row tiles they spill 2 to 18 registers, stored before the loops
+// and loaded again behind them, once a block.  384 and 2048 tokens, rank 16, groups of 32 / 64 /
+// 128: 167 / 155 / 151 and 390 / 352 / 328 us a layer, with zero points 189 / 163
+// / 156 and 454 / 376 / 344.
 #include "w4_gemm.h"
 #include "w4_launch.h"
 

@@ -1,9 +1,10 @@
 // pack_w4.hip -- quantising expert weights to 4 bits and laying them out.
 //
-// Both run once, when weights are loaded, and move every byte once: one thread
-// per output piece (pack) or per group and column (quantise), neighbouring
-// threads on neighbouring columns.  128 experts, hidden 2048, inter 768: packing
-// w13 (201 MB in and out) takes 106 us, quantising it (805 MB in) 817 us.
+// Both run once, when weights are loaded: one thread per output piece (pack) or
+// per group and column (quantise), neighbouring threads on neighbouring columns.
+// 128 experts, hidden 2048, inter 768: packing w13 (201 MB in and out) takes 106
+// us.  Quantising it takes 800 us, four times its bytes: it loads the 805 MB of
+// weights twice, for the range and for the codes, 2 bytes a thread and row.
 #include "device_common.h"
 #include "kernels_w4.h"
 #include "w4_layout.h"

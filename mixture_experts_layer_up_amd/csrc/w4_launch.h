@@ -17,11 +17,14 @@ inline int w4_local_slots(int n_slots, int E, int E_l)
 
 // Rows per work-list tile (16: few-row kernel, 32 or 64: many-row kernel), from
 // the rows an expert gets and the slots the shard gets.  Layer times in us with
-// 16 / 32 / 64 rows a tile, on 128 experts top-8 (hidden 2048, inter 768): 12
-// rows 117 / 123 / 132, 20 rows 150 / 131 / 138, 32 rows 180 / 174 / 152; with
-// fewer experts 32 rows a tile stay ahead until there are blocks enough for 64:
-// 32 local experts, 64 rows each, 142 / 111 / 124, 128 rows 220 / 276 / 150; and
-// 16 while a batch is a handful of tiles: 8 experts, 32 rows, 34 / 41 / 45.
+// 16 / 32 / 64 rows a tile (hidden 2048, inter 768, groups of 128, no LoRA), on
+// 128 experts top-8: 12 rows 93 / 99 / 109, 20 rows 117 / 102 / 112, 32 rows 139 /
+// 137 / 120, 128 rows 350 / 308 / 266.  With fewer experts 32 rows a tile stay
+// ahead until there are blocks enough for 64: 32 experts, 64 rows each, 83 / 75 /
+// 83, 128 rows 124 / 108 / 99 (96 rows, the worst choice found, 103 / 93 / 86); a
+// shard of 16 of 128 experts, 64 rows each, 73 / 60 / 66, 256 rows 178 / 120 /
+// 111.  And 16 while a batch is a handful of tiles: 8 experts, 32 rows each, 40 /
+// 45 / 51.
 inline int w4_tile_rows(int n_slots, int E, int E_l)
 {
     const int mean = n_slots / E, local = w4_local_slots(n_slots, E, E_l);
