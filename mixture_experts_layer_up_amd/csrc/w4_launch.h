@@ -55,9 +55,11 @@ inline int w4_row_tiles(int n_tiles, int n_busy, int n_local, int tile_rows)
 
 // Many-row kernel: slab groups (256 columns) that a block runs in turn on its
 // row tile, for about `tiles` row tiles with rows and n_sg groups.  As few jobs
-// per tile as still make kMinBlocks blocks (two rounds of two blocks per CU; 700
-// to 4096: the same times; 400: +38%), and the groups spread evenly over them.
-constexpr int kMinBlocks = 1024;
+// per tile as still make kMinBlocks blocks, four rounds of two blocks per CU, and
+// the groups spread evenly over them.  With 512 / 1024 / 2048 / 4096 blocks a
+// layer of 128 experts top-8 (hidden 2048, inter 768, rank 64) takes 449 / 410 /
+// 409 / 409 us at 2048 tokens and 898 / 732 / 703 / 712 at 4096.
+constexpr int kMinBlocks = 2048;
 
 inline int w4_groups_per_block(int tiles, int n_sg)
 {

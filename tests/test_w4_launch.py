@@ -41,13 +41,13 @@ int main()
 # odd number of steps; a shorter last job; column counts that end inside a group;
 # adapters.
 BLOCKS = [
-    dict(name="rows32_down", T=4000, H=4288, I=96, E=4, k=1, L=2, rg=8, rd=16, group=32, zeros=1),
-    dict(name="rows32_down_whole_jobs", T=4000, H=4608, I=128, E=4, k=1, L=2, rg=0, rd=40, group=128),
-    dict(name="rows32_gate_up", T=4000, H=320, I=2144, E=4, k=1, L=2, rg=13, rd=8, group=64, zeros=1),
-    dict(name="rows32_gate_up_even", T=4000, H=192, I=2208, E=4, k=1, L=3, rg=40, rd=0, group=128),
-    dict(name="rows64_down", T=8200, H=4288, I=64, E=3, k=1, L=2, rg=8, rd=72, group=64, zeros=1),
-    dict(name="rows64_both", T=16400, H=1280, I=608, E=4, k=2, L=2, rg=16, rd=8, group=128),
-    dict(name="rows64_gate_up", T=8200, H=320, I=2144, E=3, k=1, L=2, rg=64, rd=8, group=32, zeros=1),
+    dict(name="rows32_down", T=4000, H=8384, I=96, E=4, k=1, L=2, rg=8, rd=16, group=32, zeros=1),
+    dict(name="rows32_down_whole_jobs", T=4000, H=8704, I=128, E=4, k=1, L=2, rg=0, rd=40, group=128),
+    dict(name="rows32_gate_up", T=4000, H=320, I=4192, E=4, k=1, L=2, rg=13, rd=8, group=64, zeros=1),
+    dict(name="rows32_gate_up_even", T=4000, H=192, I=4320, E=4, k=1, L=3, rg=40, rd=0, group=128),
+    dict(name="rows64_down", T=8200, H=8384, I=64, E=3, k=1, L=2, rg=8, rd=72, group=64, zeros=1),
+    dict(name="rows64_both", T=16400, H=1792, I=864, E=4, k=2, L=2, rg=16, rd=8, group=128),
+    dict(name="rows64_gate_up", T=8200, H=320, I=4192, E=3, k=1, L=2, rg=64, rd=8, group=32, zeros=1),
 ]
 
 
@@ -70,15 +70,15 @@ def test_groups_per_block_are_even_and_make_enough_blocks(rule):
     """Jobs of one tile differ by less than the number of jobs allows: the longest
     is no longer than the mean, rounded up, and one job fewer would leave too few
     blocks."""
-    pairs = [(t, n) for t in (1, 3, 16, 60, 128, 200, 511, 512, 600, 1023, 1024, 5000) for n in range(1, 40)]
+    pairs = [(t, n) for t in (1, 3, 16, 60, 128, 200, 511, 512, 600, 1023, 1024, 2048, 5000) for n in range(1, 40)]
     for (tiles, n_sg), per in zip(pairs, rule("groups", pairs)):
         jobs = -(-n_sg // per)
         assert 1 <= per <= n_sg
         assert per == -(-n_sg // jobs), f"{tiles} tiles, {n_sg} groups: {jobs} jobs of up to {per}"
-        assert jobs == n_sg or tiles * jobs >= 1024
+        assert jobs == n_sg or tiles * jobs >= 2048
         # one job fewer, where the groups can be cut so
         fewer = [j for j in range(1, jobs) if -(-n_sg // -(-n_sg // j)) == j]
-        assert not fewer or tiles * fewer[-1] < 1024
+        assert not fewer or tiles * fewer[-1] < 2048
 
 
 def _layer(c):
@@ -111,7 +111,7 @@ def test_shards_are_cut_by_their_own_slots(rule, T, k, E, E_l):
     for (rows, tiles, per, _), a in zip(rule("layer", shard.values()), shard.values()):
         n_sg = -(-a[4] // 4)
         assert rows > 16 and tiles * rows <= max(T * k * E_l // E, E_l * rows)
-        assert per == 1 or tiles * -(-n_sg // per) >= 1024
+        assert per == 1 or tiles * -(-n_sg // per) >= 2048
 
 
 @pytest.mark.parametrize("T", [1, 2, 4, 8])
