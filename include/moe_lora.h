@@ -533,6 +533,157 @@ int moe_lora_finalize_backward(const moe_lora_shape *shape, const void *d_out, c
                                const int32_t *expanded_idx_to_permuted_idx, const float *topk_weights,
                                void *d_expert_out, float *d_topk_weights, void *stream);
 
+/*
+ * What stands around the layer in a transformer block.  The three groups below
+ * follow the conventions at the top of this file (device pointers, contiguous
+ * row-major tensors, no allocation, no host synchronisation, negative status
+ * before any HIP call, concurrent calls with distinct outputs and workspaces);
+ * workspaces are 256-byte aligned, their contents on entry do not matter, and
+ * their size depends on the shape only.  Results are the same bits in every run.
+ *
+ * Matrix product with an epilogue (the router's logits, a shared expert):
+ *   z = x w + bias,  out = act(z) + residual
+ * with x bf16 [M, K], w bf16 [K, W] (W = N; for swiglu W = 2N, columns [0, N)
+ * gate and [N, 2N) up, as in w13), bias fp32 [W] or NULL, residual bf16 [M, N]
+ * or NULL, out [M, N] bf16 or fp32.  Sums and the epilogue are fp32, rounded
+ * once.  Activations: none; relu max(z, 0); gelu z sigmoid(2 c (z + 0.044715 z^3)),
+ * c = sqrt(2 / pi) (the tanh form); silu z sigmoid(z); swiglu silu(gate) up.
+ * Limits: 0 <= M <= 2^24, K % 8 == 0, 8 <= K <= 131072, 1 <= N <= 131072,
+ * M max(K, 2N) <= 2^37.
+ */
+#define MOE_LORA_ACT_NONE   0
+#define MOE_LORA_ACT_RELU   1
+#define MOE_LORA_ACT_GELU   2
+#define MOE_LORA_ACT_SILU   3
+#define MOE_LORA_ACT_SWIGLU 4
+
+typedef struct moe_lora_linear_shape {
+    int32_t rows;           /* M */
+    int32_t in_features;    /* K */
+    int32_t out_features;   /* N */
+    int32_t activation;     /* MOE_LORA_ACT_* */
+    int32_t out_fp32;       /* type of out and d_out: 0 bf16, 1 fp32 */
+} moe_lora_linear_shape;
+
+/*
+ * preact is NULL, or receives z rounded to bf16 [M, W] (what the gradient of an
+ * activation needs).  x, w and workspace pointers 16-byte (workspace 256-byte)
+ * aligned; the others as their element type.  out may be residual itself (when it
+ * is bf16): the sum is then taken in place.  Outputs overlap nothing else.  The
+ * workspace may be NULL when its size is 0.
+ */
+size_t moe_lora_linear_workspace_size(const moe_lora_linear_shape *shape);
+
+int moe_lora_linear(const moe_lora_linear_shape *shape, const void *x, const void *w, const float *bias,
+                    const void *residual, void *out, void *preact, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of moe_lora_linear for d_out [M, N] (bf16 or fp32, as out):
+ *   dz = d_out act'(z) from preact as the forward wrote it (NULL without an
+ *   activation),  d_x = dz w^T bf16 [M, K],  d_w = x^T dz bf16 [K, W],
+ *   d_bias = sum over rows of dz, fp32 [W].
+ * Each output may be NULL, one at least is given; the residual's gradient is
+ * d_out.  dz enters the two products rounded to bf16, d_bias unrounded.  d_x
+ * needs w, d_w needs x (else they may be NULL).  With no rows, d_w and d_bias are
+ * 0.  d_x may be x itself; outputs overlap nothing else.
+ * x, w, d_out, d_x, d_w and workspace 16-byte (workspace 256-byte) aligned.
+ */
+size_t moe_lora_linear_backward_workspace_size(const moe_lora_linear_shape *shape);
+
+int moe_lora_linear_backward(const moe_lora_linear_shape *shape, const void *x, const void *w,
+                             const void *preact, const void *d_out, void *d_x, void *d_w, float *d_bias,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The norms before and after a block, with its gate and the residual sum:
+ *   b = branch / rms(branch) (weight_offset + post_weight)  (branch itself when
+ *       post_weight is NULL),
+ *   new_residual = residual_scale residual + gate b,
+ *   normed = new_residual / rms(new_residual) (weight_offset + pre_weight),
+ *   rms(v) = sqrt(mean(v^2) + eps) over the row,
+ * in fp32; both outputs are rounded once (normed comes from the unrounded sum).
+ * bf16 [T, H]: residual (NULL: 0), branch (NULL: 0; one of the two is given),
+ * new_residual and normed (NULL: not wanted; one at least is given, normed needs
+ * pre_weight).  Weights bf16 [H].  gate: MOE_LORA_GATE_NONE (NULL),
+ * MOE_LORA_GATE_TOKEN fp32 [T], MOE_LORA_GATE_CHANNEL bf16 [H].
+ * Each output may be residual or branch itself; outputs overlap nothing else.
+ * Every pointer 16-byte aligned (a token gate 4-byte).
+ * Limits: 0 <= T <= 2^24, H % 64 == 0, 64 <= H <= 65536, eps > 0.  Rows whose sum
+ * of squares passes the fp32 range (values above 1e19 / sqrt(H)) become 0.
+ */
+#define MOE_LORA_GATE_NONE    0
+#define MOE_LORA_GATE_TOKEN   1
+#define MOE_LORA_GATE_CHANNEL 2
+
+typedef struct moe_lora_norm_shape {
+    int32_t rows;           /* T */
+    int32_t hidden;         /* H */
+    float eps;
+    float residual_scale;
+    float weight_offset;    /* 0, or 1 for weights stored as w - 1 */
+    int32_t gate;           /* MOE_LORA_GATE_* */
+} moe_lora_norm_shape;
+
+int moe_lora_block_norm(const moe_lora_norm_shape *shape, const void *residual, const void *branch,
+                        const void *post_weight, const void *pre_weight, const void *gate,
+                        void *new_residual, void *normed, void *stream);
+
+/*
+ * Gradients of moe_lora_block_norm.  new_residual and branch are the forward's
+ * (bf16, as it wrote and read them), d_new_residual and d_normed bf16 [T, H] the
+ * gradients of its outputs (NULL: 0; one at least is given).  new_residual is
+ * read only with d_normed, branch only with post_weight or for d_gate.
+ * All outputs may be NULL (one at least is given):
+ *   d_residual, d_branch    bf16 [T, H]
+ *   d_post_weight, d_pre_weight  fp32 [H] (needs that weight; d_pre_weight needs
+ *                           d_normed)
+ *   d_gate                  fp32 [T] or [H] as the gate
+ * Sums over tokens are fp32 in a fixed order.  d_residual and d_branch may each be
+ * one of the four bf16 [T, H] inputs; outputs overlap nothing else.
+ */
+typedef struct moe_lora_norm_gradients {
+    void *d_residual;
+    void *d_branch;
+    float *d_post_weight;
+    float *d_pre_weight;
+    float *d_gate;
+} moe_lora_norm_gradients;
+
+size_t moe_lora_block_norm_backward_workspace_size(const moe_lora_norm_shape *shape);
+
+int moe_lora_block_norm_backward(const moe_lora_norm_shape *shape, const void *new_residual,
+                                 const void *branch, const void *post_weight, const void *pre_weight,
+                                 const void *gate, const void *d_new_residual, const void *d_normed,
+                                 const moe_lora_norm_gradients *gradients, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/*
+ * Global norm over many gradients, and clipping: norm = sqrt(sum of all squares)
+ * (fp32 [1], device; sums in 64 bits), and out = data min(1, max_norm / (norm +
+ * 1e-6)) for every tensor.  A norm that is infinite or NaN leaves the values as
+ * they are (the caller sees it in `norm`).  max_norm = infinity: the norm only,
+ * nothing is written to the tensors (`out` is not used).  `gradients` is HOST memory, read during the
+ * call; data and out are device pointers aligned to their element, out may be
+ * data (in place).  count <= 4096 tensors of 0 <= elements < 2^36 (pointers of
+ * empty ones may be NULL).  Memory ranges of two tensors must not overlap
+ * (MOE_LORA_ERR_INVALID_ARG): a tensor given twice would be counted and scaled
+ * twice.  The device addresses enter the launches, so a captured graph replays on
+ * the same tensors.
+ */
+typedef struct moe_lora_gradient {
+    const void *data;
+    void *out;
+    int64_t elements;
+    int32_t fp32;           /* 0: bf16, 1: fp32 */
+    int32_t reserved;       /* 0 */
+} moe_lora_gradient;
+
+size_t moe_lora_clip_workspace_size(const moe_lora_gradient *gradients, int32_t count);
+
+int moe_lora_clip_gradients(const moe_lora_gradient *gradients, int32_t count, float max_norm,
+                            float *norm, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Static description of a status code. */
 const char *moe_lora_strerror(int status);
 

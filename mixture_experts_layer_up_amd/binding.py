@@ -66,6 +66,29 @@ class Routing(ctypes.Structure):
         "lora_seg_offsets", "lora_seg_slots", "input_flags")]
 
 
+class LinearShape(ctypes.Structure):
+    """rows, in_features, out_features, activation (index into ``ACTIVATIONS``), out_fp32."""
+    _fields_ = [(name, ctypes.c_int32) for name in (
+        "rows", "in_features", "out_features", "activation", "out_fp32")]
+
+
+class NormShape(ctypes.Structure):
+    """rows, hidden, eps, residual_scale, weight_offset, gate (index into ``GATES``)."""
+    _fields_ = [("rows", ctypes.c_int32), ("hidden", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("weight_offset", ctypes.c_float),
+                ("gate", ctypes.c_int32)]
+
+
+class NormGradients(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in (
+        "d_residual", "d_branch", "d_post_weight", "d_pre_weight", "d_gate")]
+
+
+class Gradient(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("elements", ctypes.c_int64),
+                ("fp32", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class Inputs(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in (
         "hidden", "router_logits", "routing_bias", "topk_ids", "topk_weights", "w13_packed",
@@ -77,6 +100,8 @@ class Inputs(ctypes.Structure):
 
 NUM_STAGE_EVENTS = 7
 STATIC_SCRATCH_BYTES = 16 << 20  # MOE_LORA_STATIC_SCRATCH_BYTES
+ACTIVATIONS = ("none", "relu", "gelu", "silu", "swiglu")  # MOE_LORA_ACT_*
+GATES = ("none", "token", "channel")                      # MOE_LORA_GATE_*
 FLAG_EXPERT_ID = 1   # a given top-k id outside [-1, num_experts)
 FLAG_ADAPTER = 2     # a token_lora_mapping value outside [-1, num_loras)
 STAGE_NAMES = ("route_permute", "lora_shrink_gate_up", "gemm_gate_up_swiglu",
@@ -144,6 +169,25 @@ def load_library(path: str = LIB_PATH):
     lib.moe_lora_route_backward.restype = ctypes.c_int
     lib.moe_lora_finalize_backward.argtypes = [P(Shape), vp, vp, vp, vp, vp, vp, vp]
     lib.moe_lora_finalize_backward.restype = ctypes.c_int
+    LS, NS = P(LinearShape), P(NormShape)
+    for name in ("linear", "linear_backward", "block_norm_backward"):
+        size = getattr(lib, f"moe_lora_{name}_workspace_size")
+        size.argtypes = [NS if "norm" in name else LS]
+        size.restype = ctypes.c_size_t
+    lib.moe_lora_linear.argtypes = [LS, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.moe_lora_linear.restype = ctypes.c_int
+    lib.moe_lora_linear_backward.argtypes = [LS, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.moe_lora_linear_backward.restype = ctypes.c_int
+    lib.moe_lora_block_norm.argtypes = [NS, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.moe_lora_block_norm.restype = ctypes.c_int
+    lib.moe_lora_block_norm_backward.argtypes = [NS, vp, vp, vp, vp, vp, vp, vp, P(NormGradients), vp,
+                                                 ctypes.c_size_t, vp]
+    lib.moe_lora_block_norm_backward.restype = ctypes.c_int
+    lib.moe_lora_clip_workspace_size.argtypes = [P(Gradient), ctypes.c_int32]
+    lib.moe_lora_clip_workspace_size.restype = ctypes.c_size_t
+    lib.moe_lora_clip_gradients.argtypes = [P(Gradient), ctypes.c_int32, ctypes.c_float, vp, vp,
+                                            ctypes.c_size_t, vp]
+    lib.moe_lora_clip_gradients.restype = ctypes.c_int
     lib.moe_lora_strerror.argtypes = [ctypes.c_int]
     lib.moe_lora_strerror.restype = ctypes.c_char_p
     _lib = lib
@@ -649,6 +693,221 @@ def finalize_backward(shape: Shape, d_out: torch.Tensor, expert_out: Optional[to
             _ptr(d_topk_weights, torch.float32, (T, k), "d_topk_weights"))
     _check(_on(gpu, lambda stream: load_library().moe_lora_finalize_backward(*args, stream)))
     return d_expert_out, d_topk_weights
+
+
+def _scratch(need: int, device) -> Optional[torch.Tensor]:
+    """A workspace of `need` bytes, None for none."""
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+
+
+def linear_workspace_size(shape: LinearShape) -> int:
+    return int(load_library().moe_lora_linear_workspace_size(ctypes.byref(shape)))
+
+
+def linear_backward_workspace_size(shape: LinearShape) -> int:
+    return int(load_library().moe_lora_linear_backward_workspace_size(ctypes.byref(shape)))
+
+
+def _weight_columns(shape: LinearShape) -> int:
+    return 2 * shape.out_features if shape.activation == 4 else shape.out_features
+
+
+def linear(shape: LinearShape, x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
+           residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+           preact: Optional[torch.Tensor] = None,
+           workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``act(x w + bias) + residual`` [M, N], bf16 or (``shape.out_fp32``) fp32.
+
+    ``x`` bf16 [M, K]; ``w`` bf16 [K, W] with W = N, for swiglu 2N (gate columns, then
+    up columns); ``bias`` fp32 [W]; ``residual`` bf16 [M, N], which ``out`` may be.
+    ``preact`` (bf16 [M, W]) receives x w + bias for :func:`linear_backward`."""
+    M, K, N, W = shape.rows, shape.in_features, shape.out_features, _weight_columns(shape)
+    gpu = _one_gpu(x, w, bias, residual, out, preact, workspace)
+    kind = torch.float32 if shape.out_fp32 else torch.bfloat16
+    if out is None:
+        out = torch.empty((M, N), dtype=kind, device=x.device)
+    lib = load_library()
+    if workspace is None:
+        workspace = _scratch(lib.moe_lora_linear_workspace_size(ctypes.byref(shape)), x.device)
+    args = (ctypes.byref(shape), _ptr(x, _BF16, (M, K), "x"), _ptr(w, _BF16, (K, W), "w"),
+            _ptr(bias, torch.float32, (W,), "bias"), _ptr(residual, _BF16, (M, N), "residual"),
+            _ptr(out, kind if shape.out_fp32 else _BF16, (M, N), "out"),
+            _ptr(preact, _BF16, (M, W), "preact"), _ptr(workspace, None, None, "workspace"),
+            workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    _check(_on(gpu, lambda stream: lib.moe_lora_linear(*args, stream)))
+    return out
+
+
+def linear_backward(shape: LinearShape, x: Optional[torch.Tensor], w: Optional[torch.Tensor],
+                    d_out: torch.Tensor, preact: Optional[torch.Tensor] = None,
+                    d_x: Optional[torch.Tensor] = None, d_w: Optional[torch.Tensor] = None,
+                    d_bias: Optional[torch.Tensor] = None, x_grad: bool = True, w_grad: bool = True,
+                    bias_grad: bool = False,
+                    workspace: Optional[torch.Tensor] = None) -> Dict[str, Optional[torch.Tensor]]:
+    """Gradients of :func:`linear` for ``d_out`` [M, N] (typed as its output): ``d_x``
+    bf16 [M, K], ``d_w`` bf16 [K, W], ``d_bias`` fp32 [W], None for those not asked
+    for.  ``preact`` as the forward wrote it (None without an activation); the
+    residual's gradient is ``d_out`` itself.  ``d_x`` may be ``x``."""
+    M, K, N, W = shape.rows, shape.in_features, shape.out_features, _weight_columns(shape)
+    gpu = _one_gpu(d_out, x, w, preact, d_x, d_w, d_bias, workspace)
+    dev = d_out.device
+    if not x_grad:
+        d_x = None
+    elif d_x is None:
+        d_x = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    if not w_grad:
+        d_w = None
+    elif d_w is None:
+        d_w = torch.empty((K, W), dtype=torch.bfloat16, device=dev)
+    if not bias_grad:
+        d_bias = None
+    elif d_bias is None:
+        d_bias = torch.empty(W, dtype=torch.float32, device=dev)
+    lib = load_library()
+    if workspace is None:
+        workspace = _scratch(lib.moe_lora_linear_backward_workspace_size(ctypes.byref(shape)), dev)
+    args = (ctypes.byref(shape), _ptr(x, _BF16, (M, K), "x"), _ptr(w, _BF16, (K, W), "w"),
+            _ptr(preact, _BF16, (M, W), "preact"),
+            _ptr(d_out, torch.float32 if shape.out_fp32 else _BF16, (M, N), "d_out"),
+            _ptr(d_x, _BF16, (M, K), "d_x"), _ptr(d_w, _BF16, (K, W), "d_w"),
+            _ptr(d_bias, torch.float32, (W,), "d_bias"), _ptr(workspace, None, None, "workspace"),
+            workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    _check(_on(gpu, lambda stream: lib.moe_lora_linear_backward(*args, stream)))
+    return {"d_x": d_x, "d_w": d_w, "d_bias": d_bias}
+
+
+def _gate_arguments(shape: NormShape):
+    """Type and shape of the gate."""
+    if shape.gate == 1:
+        return torch.float32, (shape.rows,)
+    return _BF16, (shape.hidden,)
+
+
+def block_norm(shape: NormShape, residual: Optional[torch.Tensor], branch: Optional[torch.Tensor],
+               post_weight: Optional[torch.Tensor] = None, pre_weight: Optional[torch.Tensor] = None,
+               gate: Optional[torch.Tensor] = None, new_residual: Optional[torch.Tensor] = None,
+               normed: Optional[torch.Tensor] = None, residual_out: bool = True):
+    """The norms before and after a block: (``new_residual``, ``normed``), bf16 [T, H].
+
+    ``new_residual`` = residual_scale * ``residual`` + gate * b with b the ``branch``
+    (the layer's output) normed with ``post_weight`` (None: as it is); ``normed`` is
+    its norm with ``pre_weight`` (None: not wanted), the next block's input.  Weights
+    bf16 [H]; ``gate`` fp32 [T] or bf16 [H] as ``shape.gate`` says.  ``residual`` or
+    ``branch`` may be None (0), and either may be an output.  With ``residual_out``
+    False only ``normed`` is written."""
+    T, H = shape.rows, shape.hidden
+    some = residual if residual is not None else branch
+    if some is None:
+        raise MoELoRAError("residual or branch must be given")
+    gpu = _one_gpu(residual, branch, post_weight, pre_weight, gate, new_residual, normed)
+    if not residual_out:
+        new_residual = None
+    elif new_residual is None:
+        new_residual = torch.empty((T, H), dtype=torch.bfloat16, device=some.device)
+    if normed is None and pre_weight is not None:
+        normed = torch.empty((T, H), dtype=torch.bfloat16, device=some.device)
+    rows, col = (T, H), (H,)
+    args = (ctypes.byref(shape), _ptr(residual, _BF16, rows, "residual"), _ptr(branch, _BF16, rows, "branch"),
+            _ptr(post_weight, _BF16, col, "post_weight"), _ptr(pre_weight, _BF16, col, "pre_weight"),
+            _ptr(gate, *_gate_arguments(shape), "gate"), _ptr(new_residual, _BF16, rows, "new_residual"),
+            _ptr(normed, _BF16, rows, "normed"))
+    _check(_on(gpu, lambda stream: load_library().moe_lora_block_norm(*args, stream)))
+    return new_residual, normed
+
+
+def block_norm_backward_workspace_size(shape: NormShape) -> int:
+    return int(load_library().moe_lora_block_norm_backward_workspace_size(ctypes.byref(shape)))
+
+
+def block_norm_backward(shape: NormShape, new_residual: Optional[torch.Tensor],
+                        branch: Optional[torch.Tensor], post_weight: Optional[torch.Tensor] = None,
+                        pre_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                        d_residual: Optional[torch.Tensor] = None, d_normed: Optional[torch.Tensor] = None,
+                        wanted: Sequence[str] = ("residual", "branch", "post_weight", "pre_weight", "gate"),
+                        out: Optional[Dict[str, torch.Tensor]] = None,
+                        workspace: Optional[torch.Tensor] = None) -> Dict[str, Optional[torch.Tensor]]:
+    """Gradients of :func:`block_norm` for those of its outputs, ``d_residual`` and
+    ``d_normed`` (bf16 [T, H], None: 0), at ``new_residual`` as it wrote it: a dict of
+    ``residual`` and ``branch`` (bf16 [T, H]), ``post_weight``, ``pre_weight`` and
+    ``gate`` (fp32), None for what is not in ``wanted`` or has no input.  ``out`` may
+    hold tensors to write them to."""
+    T, H = shape.rows, shape.hidden
+    out = dict(out) if out else {}
+    some = d_residual if d_residual is not None else d_normed
+    if some is None:
+        raise MoELoRAError("d_residual or d_normed must be given")
+    gpu = _one_gpu(new_residual, branch, post_weight, pre_weight, gate, d_residual, d_normed, workspace,
+                   *out.values())
+    has = {"residual": True, "branch": branch is not None, "post_weight": post_weight is not None,
+           "pre_weight": pre_weight is not None and d_normed is not None, "gate": gate is not None}
+    rows, col = (T, H), (H,)
+    sizes = {"residual": rows, "branch": rows, "post_weight": col, "pre_weight": col,
+             "gate": (T,) if shape.gate == 1 else col}
+    got, ptrs = {}, []
+    for name, size in sizes.items():
+        if name not in wanted or not has[name]:
+            got[name] = None
+            ptrs.append(None)
+            continue
+        kind = torch.bfloat16 if size is rows else torch.float32
+        t = out.get(name)
+        if t is None:
+            t = torch.empty(size, dtype=kind, device=some.device)
+        got[name] = t
+        ptrs.append(_ptr(t, _BF16 if size is rows else kind, size, name + " gradient"))
+    lib = load_library()
+    if workspace is None:
+        workspace = _scratch(lib.moe_lora_block_norm_backward_workspace_size(ctypes.byref(shape)), some.device)
+    args = (ctypes.byref(shape), _ptr(new_residual, _BF16, rows, "new_residual"),
+            _ptr(branch, _BF16, rows, "branch"), _ptr(post_weight, _BF16, col, "post_weight"),
+            _ptr(pre_weight, _BF16, col, "pre_weight"), _ptr(gate, *_gate_arguments(shape), "gate"),
+            _ptr(d_residual, _BF16, rows, "d_residual"), _ptr(d_normed, _BF16, rows, "d_normed"),
+            ctypes.byref(NormGradients(*ptrs)), _ptr(workspace, None, None, "workspace"),
+            workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    _check(_on(gpu, lambda stream: lib.moe_lora_block_norm_backward(*args, stream)))
+    return got
+
+
+def _gradients(gradients: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]]):
+    """The moe_lora_gradient array of the tensors."""
+    if out is None:
+        out = gradients
+    elif len(out) != len(gradients):
+        raise MoELoRAError(f"out has {len(out)} tensors, gradients has {len(gradients)}")
+    table = (Gradient * len(gradients))()
+    for entry, g, o in zip(table, gradients, out):
+        entry.data = data = _ptr(g, (torch.bfloat16, torch.float32), None, "gradient")
+        entry.out = data if o is g else _ptr(o, g.dtype, g.shape, "out")
+        entry.elements = g.numel()
+        entry.fp32 = g.dtype is torch.float32
+    return table
+
+
+def clip_workspace_size(gradients: Sequence[torch.Tensor]) -> int:
+    return int(load_library().moe_lora_clip_workspace_size(_gradients(gradients, None), len(gradients)))
+
+
+def clip_gradients(gradients: Sequence[torch.Tensor], max_norm: float,
+                   out: Optional[Sequence[torch.Tensor]] = None, norm: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None):
+    """Scales bf16 or fp32 gradients by min(1, max_norm / (norm + 1e-6)) of their
+    global norm, in place or into ``out``: (``norm`` fp32 [1], the scaled tensors).
+    A norm that is not finite leaves the values as they are; ``max_norm`` = inf only
+    takes the norm."""
+    if not len(gradients):
+        raise MoELoRAError("no gradients given")
+    gpu = _one_gpu(*gradients, *(out if out is not None else ()), norm, workspace)
+    dev = gradients[0].device
+    table = _gradients(gradients, out)
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device=dev)
+    lib = load_library()
+    if workspace is None:
+        workspace = _scratch(lib.moe_lora_clip_workspace_size(table, len(table)), dev)
+    args = (table, len(table), max_norm, _ptr(norm, torch.float32, (1,), "norm"),
+            _ptr(workspace, None, None, "workspace"), workspace.numel() * workspace.element_size())
+    _check(_on(gpu, lambda stream: lib.moe_lora_clip_gradients(*args, stream)))
+    return norm, list(out if out is not None else gradients)
 
 
 def layer_from_host(cfg, inputs: Dict, device="cuda"):

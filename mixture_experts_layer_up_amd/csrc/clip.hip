@@ -1,0 +1,231 @@
+// clip.hip -- the global norm over many gradients, and the clipped gradients.
+//
+//   norm = sqrt(sum over all tensors of g^2),  c = min(1, max_norm / (norm + 1e-6)),
+//   out = c g
+// Memory bound: every gradient is read for the sum, and read and written for the
+// product.  A block owns a chunk of one tensor; which one it finds in the table
+// that travels as the kernel's argument, so a call needs no table in device memory
+// and a captured call replays by itself.  Squares are summed in fp64 (values of
+// any size, any count; the units for it idle otherwise) in a fixed order: threads,
+// waves, blocks.
+#include "device_common.h"
+#include "kernels_block.h"
+
+namespace moe_lora {
+namespace {
+
+constexpr int kThreads = 256;
+
+// The chunk of block `block` : tensor index, first element and elements.
+__device__ __forceinline__ int find_tensor(const ClipTable &t, int block)
+{
+    int lo = 0, hi = t.count - 1;   // the last tensor whose first block is not past `block`
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (t.t[mid].first <= block)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+template <int F32>
+struct Element;
+template <>
+struct Element<0> {
+    using type = uint16_t;
+    static __device__ float load(const uint16_t *p) { return bf16_bits_to_float(*p); }
+    static __device__ void store(uint16_t *p, float v) { *p = (uint16_t)float_to_bf16_bits(v); }
+};
+template <>
+struct Element<1> {
+    using type = float;
+    static __device__ float load(const float *p) { return *p; }
+    static __device__ void store(float *p, float v) { *p = v; }
+};
+
+// Values of a 16-byte word.
+template <int F32>
+__device__ __forceinline__ void unpack(u32x4 v, float (&f)[F32 ? 4 : 8])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (F32 != 0) {
+            f[i] = __uint_as_float(v[i]);
+        } else {
+            f[2 * i] = __uint_as_float(v[i] << 16);
+            f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+        }
+    }
+}
+
+template <int F32>
+__device__ __forceinline__ u32x4 pack(const float (&f)[F32 ? 4 : 8])
+{
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (F32 != 0)
+            v[i] = __float_as_uint(f[i]);
+        else
+            v[i] = float_to_bf16_bits(f[2 * i]) | (float_to_bf16_bits(f[2 * i + 1]) << 16);
+    }
+    return v;
+}
+
+// Elements of p before its first 16-byte boundary, at most n.
+template <int F32>
+__device__ __forceinline__ int head_of(const void *p, int n)
+{
+    constexpr int kSize = F32 ? 4 : 2;
+    const int head = (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / kSize;
+    return head < n ? head : n;
+}
+
+template <int F32>
+__device__ __forceinline__ double chunk_squares(const void *data, int64_t at, int n)
+{
+    using E = Element<F32>;
+    constexpr int kPer = F32 ? 4 : 8;
+    const auto *p = static_cast<const typename E::type *>(data) + at;
+    const int head = head_of<F32>(p, n), words = (n - head) / kPer, tail = head + words * kPer;
+    double s = 0.0;
+    if ((int)threadIdx.x < head) {
+        const double v = E::load(p + threadIdx.x);
+        s = v * v;
+    }
+    if ((int)threadIdx.x < n - tail) {
+        const double v = E::load(p + tail + threadIdx.x);
+        s = fma(v, v, s);
+    }
+#pragma unroll 4
+    for (int w = threadIdx.x; w < words; w += kThreads) {
+        float f[kPer];
+        unpack<F32>(load16(p + head + w * kPer), f);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            s = fma((double)f[i], (double)f[i], s);
+    }
+    return s;
+}
+
+template <int F32>
+__device__ __forceinline__ void chunk_scale(const void *data, void *out, int64_t at, int n, float c)
+{
+    using E = Element<F32>;
+    constexpr int kPer = F32 ? 4 : 8;
+    const auto *p = static_cast<const typename E::type *>(data) + at;
+    auto *o = static_cast<typename E::type *>(out) + at;
+    if ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15) {
+        for (int i = threadIdx.x; i < n; i += kThreads)   // 16-byte boundaries differ
+            E::store(o + i, E::load(p + i) * c);
+        return;
+    }
+    const int head = head_of<F32>(p, n), words = (n - head) / kPer, tail = head + words * kPer;
+    if ((int)threadIdx.x < head)
+        E::store(o + threadIdx.x, E::load(p + threadIdx.x) * c);
+    if ((int)threadIdx.x < n - tail)
+        E::store(o + tail + threadIdx.x, E::load(p + tail + threadIdx.x) * c);
+#pragma unroll 4
+    for (int w = threadIdx.x; w < words; w += kThreads) {
+        float f[kPer];
+        unpack<F32>(load16(p + head + w * kPer), f);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            f[i] *= c;
+        store16(o + head + w * kPer, pack<F32>(f));
+    }
+}
+
+__device__ __forceinline__ double wave_sum(double s)
+{
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1)
+        s += __shfl_xor(s, off);
+    return s;
+}
+
+__global__ __launch_bounds__(kThreads) void clip_squares_kernel(ClipTable t, double *partial)
+{
+    __shared__ double part[kThreads / kWave];
+    const int i = find_tensor(t, blockIdx.x);
+    const int64_t at = (int64_t)((int)blockIdx.x - t.t[i].first) * kClipChunk;
+    const int64_t left = t.t[i].n - at;
+    const int n = left < kClipChunk ? (int)left : kClipChunk;
+    double s = t.t[i].fp32 ? chunk_squares<1>(t.t[i].data, at, n) : chunk_squares<0>(t.t[i].data, at, n);
+    s = wave_sum(s);
+    if ((threadIdx.x & (kWave - 1)) == 0)
+        part[wave_id()] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kThreads / kWave; ++w)
+            s += part[w];
+        partial[blockIdx.x] = s;
+    }
+}
+
+constexpr int kNormThreads = 1024;
+
+__global__ __launch_bounds__(kNormThreads) void clip_norm_kernel(const double *partial, int64_t blocks,
+                                                                 float max_norm, float *norm, float *factor)
+{
+    __shared__ double part[kNormThreads / kWave];
+    double s = 0.0;
+#pragma unroll 4
+    for (int64_t b = threadIdx.x; b < blocks; b += kNormThreads)
+        s += partial[b];
+    s = wave_sum(s);
+    if ((threadIdx.x & (kWave - 1)) == 0)
+        part[wave_id()] = s;
+    __syncthreads();
+    if (threadIdx.x != 0)
+        return;
+    for (int w = 1; w < kNormThreads / kWave; ++w)
+        s += part[w];
+    const double total = sqrt(s);
+    const float rounded = (float)total;
+    *norm = rounded;
+    // a norm that is not finite (as the caller sees it): leave the values as they are
+    const double c = (double)max_norm / (total + 1e-6);
+    *factor = rounded < __builtin_inff() && c < 1.0 ? (float)c : 1.0f;
+}
+
+__global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable t, const float *factor)
+{
+    const float c = *factor;
+    const int i = find_tensor(t, blockIdx.x);
+    if (c == 1.0f && t.t[i].out == t.t[i].data)
+        return;
+    const int64_t at = (int64_t)((int)blockIdx.x - t.t[i].first) * kClipChunk;
+    const int64_t left = t.t[i].n - at;
+    const int n = left < kClipChunk ? (int)left : kClipChunk;
+    if (t.t[i].fp32)
+        chunk_scale<1>(t.t[i].data, t.t[i].out, at, n, c);
+    else
+        chunk_scale<0>(t.t[i].data, t.t[i].out, at, n, c);
+}
+
+} // namespace
+
+hipError_t launch_clip_squares(const ClipTable &t, double *partial, hipStream_t s)
+{
+    hipLaunchKernelGGL(clip_squares_kernel, dim3(t.blocks), dim3(kThreads), 0, s, t, partial);
+    return hipGetLastError();
+}
+
+hipError_t launch_clip_norm(const double *partial, int64_t blocks, float max_norm, float *norm,
+                            float *factor, hipStream_t s)
+{
+    hipLaunchKernelGGL(clip_norm_kernel, dim3(1), dim3(kNormThreads), 0, s, partial, blocks, max_norm, norm,
+                       factor);
+    return hipGetLastError();
+}
+
+hipError_t launch_clip_scale(const ClipTable &t, const float *factor, hipStream_t s)
+{
+    hipLaunchKernelGGL(clip_scale_kernel, dim3(t.blocks), dim3(kThreads), 0, s, t, factor);
+    return hipGetLastError();
+}
+
+} // namespace moe_lora
