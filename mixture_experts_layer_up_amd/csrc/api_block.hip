@@ -89,7 +89,7 @@ struct ForwardLayout {
         weight = partial = total = 0;
         if (z.M == 0 || rows)
             return;
-        plan = plan_product(Product::forward, z.M, z.columns(), z.K, z.gated);
+        plan = plan_product(z.M, z.columns(), z.K, z.gated);
         partial = z.padded() ? align_up((size_t)z.K * z.columns() * 2) : 0;
         total = partial + split_bytes(plan, z.M, z.columns());
     }
@@ -103,8 +103,8 @@ struct BackwardLayout {
     explicit BackwardLayout(const Sizes &z, const moe_lora_linear_shape *s)
     {
         const int64_t M = std::max<int64_t>(z.M, 1);
-        dx = plan_product(Product::input_grad, M, z.K, z.columns(), false);
-        dw = plan_product(Product::weight_grad, z.K, z.columns(), M, false);
+        dx = plan_product(M, z.K, z.columns(), false);
+        dw = plan_product(z.K, z.columns(), M, false);
         strips = act_grad_blocks(z.M, z.N);
         makes_dz = s->activation != MOE_LORA_ACT_NONE || s->out_fp32 || z.padded();
         size_t o = 0;
@@ -124,8 +124,8 @@ struct BackwardLayout {
 
 bool wide_epilogue(const Epilogue &e)
 {
-    return e.N % 4 == 0 && aligned(e.bias, 16) && aligned(e.residual, 8) && aligned(e.preact, 8) &&
-           aligned(e.out, e.fp32 ? 16 : 8);
+    return e.N % 8 == 0 && aligned(e.bias, 16) && aligned(e.residual, 16) && aligned(e.preact, 16) &&
+           aligned(e.out, 16);
 }
 
 // ---- norms ----------------------------------------------------------------

@@ -37,12 +37,23 @@ __device__ __forceinline__ void buffer_load_lds16(u32x4 resource, uint32_t offse
                  : "memory");
 }
 
-// Every load of this wave has landed and its LDS reads are done; then the block meets.
+// At most N of this wave's loads are still to land and its LDS reads are done; then
+// the block meets.
+template <int N>
 __device__ __forceinline__ void landed_barrier()
 {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    static_assert(N < 64, "the counter has 6 bits");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(N) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+}
+
+// LDS that only this wave uses: its stores are done before its loads that follow (the
+// hardware keeps a wave's LDS operations in order; this keeps the compiler's).
+__device__ __forceinline__ void lds_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
 }
 
 } // namespace moe_lora

@@ -24,7 +24,7 @@ struct Epilogue {
     int sets;                  // 1, or 2: the stored row has W = sets N columns
     int act;                   // MOE_LORA_ACT_*
     int fp32;                  // type of out
-    int wide;                  // N and every pointer allow four elements at once
+    int wide;                  // N and every pointer allow eight elements at once
     int padded;                // gradient of a padded weight: columns [N, half) are dropped
 };
 
@@ -53,7 +53,7 @@ struct ProductPlan {
     int tile;      // index of the tile shape
     int tiles_m, tiles_n, splits, k_per;
 };
-ProductPlan plan_product(Product kind, int64_t M, int64_t C, int64_t K, bool gated);
+ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated);
 hipError_t launch_product(Product kind, const ProductPlan &plan, const ProductArgs &a, hipStream_t s);
 
 // The forward product for few rows: the weight as given, any N.

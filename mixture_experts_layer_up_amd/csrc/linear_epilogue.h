@@ -62,67 +62,82 @@ __device__ __forceinline__ void finish_one(const Epilogue &e, int64_t m, int n, 
         static_cast<uint16_t *>(e.out)[at] = (uint16_t)float_to_bf16_bits(z);
 }
 
-__device__ __forceinline__ uint2 pack4(const float (&f)[4])
+// finish_one where the row and the column of the product exist.
+__device__ __forceinline__ void finish_element(const Epilogue &e, int M, int64_t m, int c, float z, float up)
 {
-    return uint2{float_to_bf16_bits(f[0]) | (float_to_bf16_bits(f[1]) << 16),
-                 float_to_bf16_bits(f[2]) | (float_to_bf16_bits(f[3]) << 16)};
+    if (m >= M)
+        return;
+    if (e.padded) {
+        const int at = stored_column(e, c);
+        if (at >= 0)
+            static_cast<uint16_t *>(e.out)[m * e.sets * e.N + at] = (uint16_t)float_to_bf16_bits(z);
+    } else if (c < e.N) {
+        finish_one(e, m, c, z, up);
+    }
 }
 
-// Four outputs n .. n + 3 of row m, n a multiple of 4.  Where N is a multiple of 4
-// and the pointers allow it (`wide`).
-__device__ __forceinline__ void finish_four(const Epilogue &e, int64_t m, int n, float (&z)[4], float (&up)[4])
+__device__ __forceinline__ u32x4 pack_eight(const float (&f)[8])
 {
-    if (e.padded) {
+    u32x4 v;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = stored_column(e, n + i);
-            if (c >= 0)
-                static_cast<uint16_t *>(e.out)[m * e.sets * e.N + c] = (uint16_t)float_to_bf16_bits(z[i]);
-        }
-        return;
-    }
-    if (n >= e.N)
-        return;
-    if (!e.wide) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (n + i < e.N)
-                finish_one(e, m, n + i, z[i], up[i]);
-        return;
-    }
+    for (int i = 0; i < 4; ++i)
+        v[i] = float_to_bf16_bits(f[2 * i]) | (float_to_bf16_bits(f[2 * i + 1]) << 16);
+    return v;
+}
+
+// Eight outputs n .. n + 7 of row m, 16 bytes at a time: `wide` (N and n are multiples
+// of 8), n < N.
+__device__ __forceinline__ void finish_eight(const Epilogue &e, int64_t m, int n, float (&z)[8], float (&up)[8])
+{
     const int64_t at = m * e.N + n;
     const bool gated = e.act == MOE_LORA_ACT_SWIGLU;
     if (e.bias) {
-        const float4 b = *reinterpret_cast<const float4 *>(e.bias + n);
-        z[0] += b.x, z[1] += b.y, z[2] += b.z, z[3] += b.w;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            z[i] += e.bias[n + i];
         if (gated) {
-            const float4 u = *reinterpret_cast<const float4 *>(e.bias + e.N + n);
-            up[0] += u.x, up[1] += u.y, up[2] += u.z, up[3] += u.w;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                up[i] += e.bias[e.N + n + i];
         }
     }
     if (e.preact) {
-        *reinterpret_cast<uint2 *>(e.preact + (gated ? 2 * m * e.N + n : at)) = pack4(z);
+        store16(e.preact + (gated ? 2 * m * e.N + n : at), pack_eight(z));
         if (gated)
-            *reinterpret_cast<uint2 *>(e.preact + (2 * m + 1) * e.N + n) = pack4(up);
+            store16(e.preact + (2 * m + 1) * e.N + n, pack_eight(up));
     }
     if (gated) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 8; ++i)
             z[i] = silu_f32(z[i]) * up[i];
-    } else if (e.act != MOE_LORA_ACT_NONE) {
+    } else if (e.act == MOE_LORA_ACT_RELU) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            z[i] = activate(e.act, z[i]);
+        for (int i = 0; i < 8; ++i)
+            z[i] = activate(MOE_LORA_ACT_RELU, z[i]);
+    } else if (e.act == MOE_LORA_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            z[i] = activate(MOE_LORA_ACT_GELU, z[i]);
+    } else if (e.act == MOE_LORA_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            z[i] = silu_f32(z[i]);
     }
     if (e.residual) {
-        const uint2 r = *reinterpret_cast<const uint2 *>(e.residual + at);
-        z[0] += bf16_bits_to_float(r.x & 0xffffu), z[1] += bf16_bits_to_float(r.x >> 16);
-        z[2] += bf16_bits_to_float(r.y & 0xffffu), z[3] += bf16_bits_to_float(r.y >> 16);
+        const u32x4 r = load16(e.residual + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            z[2 * i] += __uint_as_float(r[i] << 16);
+            z[2 * i + 1] += __uint_as_float(r[i] & 0xffff0000u);
+        }
     }
-    if (e.fp32)
-        *reinterpret_cast<float4 *>(static_cast<float *>(e.out) + at) = float4{z[0], z[1], z[2], z[3]};
-    else
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(e.out) + at) = pack4(z);
+    if (e.fp32) {
+        float *o = static_cast<float *>(e.out) + at;
+        *reinterpret_cast<f32x4 *>(o) = f32x4{z[0], z[1], z[2], z[3]};
+        *reinterpret_cast<f32x4 *>(o + 4) = f32x4{z[4], z[5], z[6], z[7]};
+    } else {
+        store16(static_cast<uint16_t *>(e.out) + at, pack_eight(z));
+    }
 }
 
 } // namespace

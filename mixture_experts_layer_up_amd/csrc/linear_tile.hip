@@ -6,9 +6,10 @@
 // the transposing read, so no operand is laid out anew.
 //
 // A block owns a tile of BM rows and BN columns.  Steps of 64 terms of both
-// operands go through two LDS buffers, written by direct global->LDS loads that
-// run under the MFMAs of the step before.  D = P^T Q^T tiles: a lane then holds
-// four neighbouring columns of one row, which the epilogue stores at once.
+// operands go through a ring of STAGES LDS buffers, written by direct global->LDS
+// loads; the fragments of 32 terms are read from LDS under the MFMAs of the 32
+// before, so a buffer is free for the loads after next half way through its step.  The fragments give
+// D^T: a lane holds four neighbouring columns of one row.
 #include "block_dma.h"
 #include "device_common.h"
 #include "kernels_block.h"
@@ -17,8 +18,6 @@
 namespace moe_lora {
 namespace {
 
-constexpr int kStep = 64;   // terms of a step
-
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
@@ -26,10 +25,16 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 // columns) by 64 terms, R * 128 bytes.
 //  Contiguous: outer index r at r * 128, its eight 16-byte pieces of 8 terms
 //    XOR-swizzled by bits 1..3 of r, so that the 16 rows x 16 bytes of a fragment
-//    read meet every bank once.
+//    read meet every bank once.  A row's share of a step is a whole 128-byte line:
+//    with steps of 32 terms the loads alone took 81 us instead of 71 for 8192 x 2048
+//    outputs of 4096 terms.
 //  Strided: term k at k * 2R, its 32-byte units of 16 outer indices XOR-swizzled by
 //    bits 0, 1 and 3 of k: a transposing read takes 32 bytes of 16 terms, 8 of them
 //    a half wave, which then meet every bank once.
+constexpr int BK = 64;   // terms of a step
+
+__device__ __forceinline__ int piece_swizzle(int r) { return (r >> 1) & 7; }
+
 template <int R>
 __device__ __forceinline__ int unit_swizzle(int k)
 {
@@ -39,10 +44,11 @@ __device__ __forceinline__ int unit_swizzle(int k)
         return (k & 3) | ((k >> 1) & 4);
 }
 
-// Addresses of the direct loads of one operand: NT threads, R / 8 * 64 / NT pieces each.
+// Addresses of the direct loads of one operand: NT threads, R * BK / 8 / NT pieces each.
 template <int R, int NT, bool STRIDED>
 struct Loader {
-    static constexpr int kLoads = R * 8 / NT;
+    static constexpr int kLoads = R * BK / 8 / NT;
+    static_assert(kLoads * NT * 8 == R * BK, "whole pieces for every thread");
     uint32_t offset[kLoads];   // bytes from the step's base; kNone: reads as zeros
     int term[kLoads];          // first term of the piece, within the step
 
@@ -62,7 +68,8 @@ struct Loader {
                 term[i] = k;
                 offset[i] = c < 0 ? kNone : (uint32_t)(k * ld + c) * 2u;
             } else {
-                const int r = piece >> 3, q = (piece & 7) ^ ((r >> 1) & 7);
+                constexpr int kPieces = BK / 8;
+                const int r = piece / kPieces, q = (piece % kPieces) ^ piece_swizzle(r);
                 term[i] = q * 8;
                 offset[i] = first + r < count ? (uint32_t)(r * ld + q * 8) * 2u : kNone;
             }
@@ -70,15 +77,13 @@ struct Loader {
     }
 
     // `left`: terms that remain from the step's first on
-    __device__ __forceinline__ void issue(u32x4 resource, uint32_t lds, int left)
+    __device__ __forceinline__ void issue(int i, u32x4 resource, uint32_t lds, int left) const
     {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            buffer_load_lds16(resource, term[i] < left ? offset[i] : kNone, lds + i * NT * 16);
+        buffer_load_lds16(resource, term[i] < left ? offset[i] : kNone, lds + i * NT * 16);
     }
 };
 
-// MFMA operand fragment of 16 outer indices and 32 terms (half h of the step).
+// MFMA operand fragment of 16 outer indices and 32 terms (half h of a step).
 template <int R, bool STRIDED>
 __device__ __forceinline__ u32x4 fragment(const char *tile, int sixteen, int h, int lane)
 {
@@ -93,20 +98,31 @@ __device__ __forceinline__ u32x4 fragment(const char *tile, int sixteen, int h, 
         return u32x4{lo.x, lo.y, hi.x, hi.y};
     } else {
         const int r = sixteen * 16 + i;
-        return *reinterpret_cast<const u32x4 *>(tile + r * 128 + (((4 * h + g) ^ ((r >> 1) & 7)) * 16));
+        return *reinterpret_cast<const u32x4 *>(tile + r * BK * 2 + ((4 * h + g) ^ piece_swizzle(r)) * 16);
     }
 }
 
-// WM x WN waves share the tile; GATED: columns are swiglu pairs, the tile's units
-// of 16 alternate gate and up columns, BN / 2 outputs wide.
-template <int BM, int BN, int WM, int WN, bool QS, bool PS, bool GATED, bool SPLIT>
-__global__ __launch_bounds__(WM *WN * 64, BM * BN * WM * WN >= 256 * 256 * 8 ? 2 : 2)
-void product_kernel(ProductArgs a)
+enum Store {
+    kPartial,  // fp32 sums of a split
+    kPlain,    // bf16, nothing else, C a multiple of 8
+    kFull,     // the epilogue
+    kGated     // the epilogue of swiglu pairs: the tile's units of 16 columns alternate gate
+               // and up, it is BN / 2 outputs wide
+};
+
+// WM x WN waves share the tile.
+template <int BM, int BN, int STAGES, int WM, int WN, bool QS, bool PS, Store STORE>
+__global__ __launch_bounds__(WM *WN * 64, 2) void product_kernel(ProductArgs a)
 {
+    constexpr bool GATED = STORE == kGated;
     constexpr int NT = WM * WN * 64;
-    constexpr int kQ = BM * 128, kP = BN * 128, kBuffer = kQ + kP;
+    constexpr int kQ = BM * BK * 2, kP = BN * BK * 2, kBuffer = kQ + kP;
     constexpr int MT = BM / WM / 16, NTL = BN / WN / 16;
-    __shared__ __attribute__((aligned(1024))) char lds[2 * kBuffer];
+    constexpr int kSlab = MT * 16 < 64 ? MT * 16 : 64;   // rows a wave turns around at once
+    constexpr int kTurn = NTL * 16 + 4;                  // floats of such a row: banks shift by 4 a row
+    constexpr int kTurns = WM * WN * kSlab * kTurn * 4;
+    constexpr int kRing = STAGES * kBuffer;
+    __shared__ __attribute__((aligned(1024))) char lds[kRing > kTurns ? kRing : kTurns];
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
 
     // consecutive tiles of one XCD are neighbours in both directions
@@ -123,7 +139,7 @@ void product_kernel(ProductArgs a)
     const int m0 = tm * BM, n0 = tn * (GATED ? BN / 2 : BN);
     const int k0 = split * a.k_per;
     const int K = a.K - k0 < a.k_per ? a.K - k0 : a.k_per;
-    const int steps = (K + kStep - 1) / kStep;
+    const int steps = (K + BK - 1) / BK;
 
     // rows a tile does not have read as zeros
     Loader<BM, NT, QS> lq;
@@ -143,14 +159,25 @@ void product_kernel(ProductArgs a)
     });
     const char *q = reinterpret_cast<const char *>(a.Q + (QS ? (size_t)k0 * a.ldq + m0 : (size_t)m0 * a.ldq + k0));
     const char *p = reinterpret_cast<const char *>(a.P + (PS ? (size_t)k0 * a.ldp + n0 : (size_t)n0 * a.ldp + k0));
-    const size_t q_step = QS ? (size_t)kStep * a.ldq * 2 : kStep * 2;
-    const size_t p_step = PS ? (size_t)kStep * a.ldp * 2 : kStep * 2;
+    const size_t q_step = QS ? (size_t)BK * a.ldq * 2 : BK * 2;
+    const size_t p_step = PS ? (size_t)BK * a.ldp * 2 : BK * 2;
     const uint32_t base = lds_base(lds) + wave * 1024;
 
-    auto issue = [&](int s) {
-        const uint32_t at = base + (s & 1) * kBuffer;
-        lq.issue(buffer_resource(q + s * q_step), at, K - s * kStep);
-        lp.issue(buffer_resource(p + s * p_step), at + kQ, K - s * kStep);
+    // loads of a step past the last read nothing and write zeros: the waits stay the same
+    constexpr int kLoads = lq.kLoads + lp.kLoads;
+    int next = 0, next_at = 0;
+    auto issue = [&](int i) {
+        const int left = K - next * BK;
+        if (i < lq.kLoads)
+            lq.issue(i, buffer_resource(q), base + next_at, left);
+        else
+            lp.issue(i - lq.kLoads, buffer_resource(p), base + next_at + kQ, left);
+        if (i == kLoads - 1) {
+            q += q_step;
+            p += p_step;
+            ++next;
+            next_at = next_at + kBuffer == kRing ? 0 : next_at + kBuffer;
+        }
     };
 
     f32x4 acc[MT][NTL];
@@ -161,55 +188,108 @@ void product_kernel(ProductArgs a)
             acc[m][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const int wm = wave / WN * MT, wn = wave % WN * NTL;   // in sixteens
 
-    issue(0);
-    landed_barrier();
-    for (int s = 0; s < steps; ++s) {
-        if (s + 1 < steps)
-            issue(s + 1);
-        const char *tq = lds + (s & 1) * kBuffer, *tp = tq + kQ;
+    struct Fragments {
+        u32x4 p[NTL], q[MT];
+    };
+    Fragments one, two;
+    int at = 0;
+    auto read_p = [&](Fragments &f, int n, int h) { f.p[n] = fragment<BN, PS>(lds + at + kQ, wn + n, h, lane); };
+    auto read_q = [&](Fragments &f, int m, int h) { f.q[m] = fragment<BM, QS>(lds + at, wm + m, h, lane); };
+    // The products of one half step, between them the reads of the next and, after the
+    // barrier, the loads.  The scheduling barriers keep them there: left alone, the reads
+    // sink to their uses.
+    auto half = [&](const Fragments &now, Fragments &after, int h, bool load) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            u32x4 fp[NTL];
+        for (int m = 0; m < MT; ++m) {
+#pragma unroll
+            for (int n = m * NTL / MT; n < (m + 1) * NTL / MT; ++n)
+                read_p(after, n, h);
+            read_q(after, m, h);
+            if (load)
+#pragma unroll
+                for (int i = m * kLoads / MT; i < (m + 1) * kLoads / MT; ++i)
+                    issue(i);
 #pragma unroll
             for (int n = 0; n < NTL; ++n)
-                fp[n] = fragment<BN, PS>(tp, wn + n, h, lane);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const u32x4 fq = fragment<BM, QS>(tq, wm + m, h, lane);
-#pragma unroll
-                for (int n = 0; n < NTL; ++n)
-                    acc[m][n] = mfma_16x16x32(fp[n], fq, acc[m][n]);
-            }
+                acc[m][n] = mfma_16x16x32(now.p[n], now.q[m], acc[m][n]);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        landed_barrier();
+    };
+#pragma unroll
+    for (int st = 0; st < STAGES; ++st)
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            issue(i);
+    landed_barrier<(STAGES - 1) * kLoads>();
+#pragma unroll
+    for (int n = 0; n < NTL; ++n)
+        read_p(one, n, 0);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+        read_q(one, m, 0);
+    for (int s = 0; s < steps; ++s) {
+        half(one, two, 1, false);
+        at = at + kBuffer == kRing ? 0 : at + kBuffer;
+        // the next step has landed, and every wave holds the rest of this one in registers
+        landed_barrier<(STAGES - 2) * kLoads>();
+        half(two, one, 0, true);
     }
+    landed_barrier<0>();
 
+    // Each wave turns its part around in LDS of its own (the last barrier has freed it),
+    // kSlab rows at a time, so that a lane finishes eight neighbouring columns and the
+    // finishing code is there once: unrolled over the fragments it missed the instruction
+    // cache for 40 us a block.
+    float *turn = reinterpret_cast<float *>(lds) + wave * kSlab * kTurn;
     const int i = lane & 15, g = lane >> 4;
+    constexpr int kOut = GATED ? NTL * 8 : NTL * 16;   // outputs of a row of the wave's part
+    constexpr int kLanes = kOut / 8, kAtOnce = 64 / kLanes;
+    const int mine = lane / kLanes, c = lane % kLanes * 8;
+    // swiglu: output columns c .. c + 7 lie in the gate unit c / 16 * 2, the up unit follows
+    const int z_at = GATED ? (c >> 4) * 32 + (c & 15) : c;
+    const int column = n0 + wn * (GATED ? 8 : 16) + c;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int64_t row = m0 + (wm + m) * 16 + i;
-        if (row >= a.M)
-            continue;
-        if constexpr (SPLIT) {
-            float *out = a.partial + ((size_t)split * a.M + row) * a.C;
+    for (int slab = 0; slab < MT * 16 / kSlab; ++slab) {
 #pragma unroll
-            for (int n = 0; n < NTL; ++n) {
-                const int c = n0 + (wn + n) * 16 + 4 * g;
-                if (c < a.C)   // C is a multiple of 8
-                    *reinterpret_cast<f32x4 *>(out + c) = acc[m][n];
+        for (int m = 0; m < kSlab / 16; ++m)
+#pragma unroll
+            for (int n = 0; n < NTL; ++n)
+                *reinterpret_cast<f32x4 *>(turn + (m * 16 + i) * kTurn + n * 16 + 4 * g) =
+                    acc[slab * (kSlab / 16) + m][n];
+        lds_order();
+        const int first = m0 + wm * 16 + slab * kSlab;
+        if (STORE >= kFull && !a.e.wide) {   // element by element, neighbours side by side
+#pragma unroll 1
+            for (int x = lane; x < kSlab * kOut; x += 64) {
+                const int r = x / kOut, o = x % kOut;
+                const float *from = turn + r * kTurn + (GATED ? (o >> 4) * 32 + (o & 15) : o);
+                finish_element(a.e, a.M, first + r, n0 + wn * (GATED ? 8 : 16) + o, from[0], GATED ? from[16] : 0.0f);
             }
         } else {
+#pragma unroll 1
+            for (int r = mine; r < kSlab; r += kAtOnce) {
+                const int64_t row = first + r;
+                if (row >= a.M || column >= (GATED ? a.e.half : a.C))
+                    break;
+                const float *from = turn + r * kTurn + z_at;
+                float z[8], up[8];
 #pragma unroll
-            for (int n = 0; n < NTL; n += GATED ? 2 : 1) {
-                float z[4], up[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    z[j] = acc[m][n][j];
-                    up[j] = GATED ? acc[m][n + (GATED ? 1 : 0)][j] : 0.0f;
+                for (int j = 0; j < 8; ++j) {
+                    z[j] = from[j];
+                    up[j] = GATED ? from[16 + j] : 0.0f;
                 }
-                finish_four(a.e, row, n0 + (GATED ? (wn + n) / 2 : wn + n) * 16 + 4 * g, z, up);
+                if constexpr (STORE == kPartial) {
+                    float *out = a.partial + ((size_t)split * a.M + row) * a.C + column;
+                    *reinterpret_cast<f32x4 *>(out) = f32x4{z[0], z[1], z[2], z[3]};
+                    *reinterpret_cast<f32x4 *>(out + 4) = f32x4{z[4], z[5], z[6], z[7]};
+                } else if constexpr (STORE == kPlain) {
+                    store16(static_cast<uint16_t *>(a.e.out) + row * a.C + column, pack_eight(z));
+                } else {
+                    finish_eight(a.e, row, column, z, up);
+                }
             }
         }
+        lds_order();
     }
 }
 
@@ -218,54 +298,88 @@ __global__ __launch_bounds__(256) void join_kernel(ProductArgs a)
 {
     const bool gated = a.e.act == MOE_LORA_ACT_SWIGLU;
     const int width = gated ? a.e.half : a.C;
-    const int per_row = width / 4;
+    const size_t apart = (size_t)a.M * a.C;
+    if (!a.e.wide) {
+        const int64_t items = (int64_t)a.M * width;
+        for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < items; x += (int64_t)gridDim.x * 256) {
+            const int64_t m = x / width;
+            const int c = (int)(x - m * width);
+            const float *in = a.partial + m * a.C + c;
+            float z = 0.0f, up = 0.0f;
+#pragma unroll 4
+            for (int s = 0; s < a.splits; ++s) {
+                z += in[s * apart];
+                if (gated)
+                    up += in[s * apart + a.e.half];
+            }
+            finish_element(a.e, a.M, m, c, z, up);
+        }
+        return;
+    }
+    const int per_row = width / 8;
     const int64_t items = (int64_t)a.M * per_row;
     for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < items; x += (int64_t)gridDim.x * 256) {
         const int64_t m = x / per_row;
-        const int n = (int)(x - m * per_row) * 4;
+        const int n = (int)(x - m * per_row) * 8;
         const float *in = a.partial + m * a.C + n;
-        f32x4 z = {}, up = {};
+        float z[8] = {}, up[8] = {};
 #pragma unroll 4
-        for (int s = 0; s < a.splits; ++s) {
-            z += *reinterpret_cast<const f32x4 *>(in + (size_t)s * a.M * a.C);
-            if (gated)
-                up += *reinterpret_cast<const f32x4 *>(in + (size_t)s * a.M * a.C + a.e.half);
+        for (int s = 0; s < a.splits; ++s)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                z[i] += in[s * apart + i];
+        if (gated) {
+            in += a.e.half;
+#pragma unroll 4
+            for (int s = 0; s < a.splits; ++s)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    up[i] += in[s * apart + i];
         }
-        float zs[4] = {z[0], z[1], z[2], z[3]}, us[4] = {up[0], up[1], up[2], up[3]};
-        finish_four(a.e, m, n, zs, us);
+        finish_eight(a.e, m, n, z, up);
     }
 }
 
+// Tile shapes, and the microseconds that a step of 64 terms takes a block alone on its
+// CU (most CUs busy) and among others there, measured with 2048 to 8192 rows, 1536 to
+// 4096 columns and as many terms.  Larger tiles read LDS and the second-level cache
+// less per product; smaller ones fill the chip with fewer rows.
 struct Tile {
     int rows, columns;
+    float alone, shared;
 };
-constexpr Tile kTiles[] = {{256, 256}, {128, 128}, {64, 64}};
+constexpr Tile kTiles[] = {{256, 256, 1.15f, 1.45f}, {256, 128, 0.65f, 0.92f}, {128, 128, 0.55f, 0.42f},
+                           {64, 64, 0.20f, 0.20f}};
+constexpr int kCus = 256;
 
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int STAGES, int WM, int WN>
 hipError_t launch_tile(Product kind, const ProductArgs &a, hipStream_t s)
 {
     const bool gated = kind == Product::forward && a.e.act == MOE_LORA_ACT_SWIGLU;
+    const bool plain = kind != Product::forward && a.e.wide && !a.e.padded;
     const int64_t items = (int64_t)a.tiles_m * a.tiles_n * a.splits;
     const dim3 grid((items + 7) / 8 * 8), block(WM * WN * 64);
-#define MOE_LAUNCH(QS, PS, GATED, SPLIT) \
-    hipLaunchKernelGGL((product_kernel<BM, BN, WM, WN, QS, PS, GATED, SPLIT>), grid, block, 0, s, a)
+#define MOE_LAUNCH(QS, PS, STORE) \
+    hipLaunchKernelGGL((product_kernel<BM, BN, STAGES, WM, WN, QS, PS, STORE>), grid, block, 0, s, a)
     if (kind == Product::forward) {
         if (a.splits > 1)
-            MOE_LAUNCH(false, true, false, true);
+            MOE_LAUNCH(false, true, kPartial);
         else if (gated)
-            MOE_LAUNCH(false, true, true, false);
+            MOE_LAUNCH(false, true, kGated);
         else
-            MOE_LAUNCH(false, true, false, false);
-    } else if (kind == Product::input_grad) {
+            MOE_LAUNCH(false, true, kFull);
+    } else if (kind == Product::input_grad) {   // always plain: K is a multiple of 8
         if (a.splits > 1)
-            MOE_LAUNCH(false, false, false, true);
+            MOE_LAUNCH(false, false, kPartial);
         else
-            MOE_LAUNCH(false, false, false, false);
+            MOE_LAUNCH(false, false, kPlain);
     } else {
         if (a.splits > 1)
-            MOE_LAUNCH(true, true, false, true);
+            MOE_LAUNCH(true, true, kPartial);
+        else if (plain)
+            MOE_LAUNCH(true, true, kPlain);
         else
-            MOE_LAUNCH(true, true, false, false);
+            MOE_LAUNCH(true, true, kFull);
     }
 #undef MOE_LAUNCH
     return hipGetLastError();
@@ -273,33 +387,45 @@ hipError_t launch_tile(Product kind, const ProductArgs &a, hipStream_t s)
 
 } // namespace
 
-ProductPlan plan_product(Product kind, int64_t M, int64_t C, int64_t K, bool gated)
+// The tile and split that take the least time by the figures above.  A split's fp32
+// sums are written and read again, at about 5 TB/s, and a second kernel starts after
+// the first (3 us): 2048 x 1536 sums of 8192 terms take 87 us whole (128 x 128 tiles),
+// 61 us as two splits of 256 x 128 tiles, 83 us as six.
+ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated)
 {
-    auto tiles_of = [&](const Tile &t) { return ((M + t.rows - 1) / t.rows) * ((C + t.columns - 1) / t.columns); };
-    int tile = 2;
-    if (tiles_of(kTiles[0]) >= 192)
-        tile = 0;
-    else if (tiles_of(kTiles[1]) >= 128)
-        tile = 1;
-    ProductPlan p{};
-    p.tile = tile;
-    const int64_t tiles = tiles_of(kTiles[tile]);
-    int64_t splits = 1;
-    if (tiles < 192) {
-        splits = 512 / tiles;
-        const int64_t most = K / 256;   // four steps a split at least
-        splits = splits < most ? splits : most;
-        splits = splits < 1 ? 1 : splits;
+    const int64_t steps = (K + BK - 1) / BK;
+    ProductPlan best{};
+    float least = 0.0f;
+    for (int t = 0; t < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++t) {
+        const Tile &tile = kTiles[t];
+        const int64_t tiles = ((M + tile.rows - 1) / tile.rows) * ((C + tile.columns - 1) / tile.columns);
+        int64_t last = 0;
+        for (int64_t splits = 1; splits <= 64; ++splits) {
+            const int64_t per = (steps + splits - 1) / splits;
+            if (splits > 1 && (per < 4 || tiles * splits > 4 * kCus))
+                break;
+            if (per == last)   // the same cutting with empty splits
+                continue;
+            last = per;
+            const int64_t each = (tiles * splits + kCus - 1) / kCus;   // blocks of the busiest CU
+            float us = per * (each == 1 ? tile.alone : each * tile.shared);
+            if (splits > 1)
+                us += 3.0f + (float)splits * M * C * 8.0f / 5e6f;
+            if (best.tiles_m == 0 || us < least) {
+                least = us;
+                best.tile = t;
+                best.splits = (int)((steps + per - 1) / per);
+                best.k_per = (int)(per * BK);
+                const bool pairs = gated && best.splits == 1;
+                const int64_t width = pairs ? C / 2 : C, columns = pairs ? tile.columns / 2 : tile.columns;
+                best.tiles_m = (int)((M + tile.rows - 1) / tile.rows);
+                best.tiles_n = (int)((width + columns - 1) / columns);
+            }
+        }
     }
-    const int64_t steps = (K + kStep - 1) / kStep;
-    const int64_t per = (steps + splits - 1) / splits;
-    p.splits = (int)((steps + per - 1) / per);
-    p.k_per = (int)(per * kStep);
-    const bool pairs = gated && p.splits == 1;
-    p.tiles_m = (int)((M + kTiles[tile].rows - 1) / kTiles[tile].rows);
-    const int64_t width = pairs ? C / 2 : C, columns = pairs ? kTiles[tile].columns / 2 : kTiles[tile].columns;
-    p.tiles_n = (int)((width + columns - 1) / columns);
-    return p;
+    if (best.splits < 1)   // no terms
+        best.splits = 1;
+    return best;
 }
 
 hipError_t launch_product(Product kind, const ProductPlan &plan, const ProductArgs &given, hipStream_t s)
@@ -309,13 +435,14 @@ hipError_t launch_product(Product kind, const ProductPlan &plan, const ProductAr
     a.tiles_n = plan.tiles_n;
     a.splits = plan.splits;
     a.k_per = plan.k_per;
-    hipError_t rc = plan.tile == 0   ? launch_tile<256, 256, 2, 4>(kind, a, s)
-                    : plan.tile == 1 ? launch_tile<128, 128, 2, 2>(kind, a, s)
-                                     : launch_tile<64, 64, 2, 2>(kind, a, s);
+    hipError_t rc = plan.tile == 0   ? launch_tile<256, 256, 2, 2, 4>(kind, a, s)
+                    : plan.tile == 1 ? launch_tile<256, 128, 3, 4, 2>(kind, a, s)
+                    : plan.tile == 2 ? launch_tile<128, 128, 2, 2, 2>(kind, a, s)
+                                     : launch_tile<64, 64, 4, 2, 2>(kind, a, s);
     if (rc != hipSuccess || a.splits == 1)
         return rc;
     const bool gated = kind == Product::forward && a.e.act == MOE_LORA_ACT_SWIGLU;
-    const int64_t items = (int64_t)a.M * ((gated ? a.e.half : a.C) / 4);
+    const int64_t items = (int64_t)a.M * (gated ? a.e.half : a.C) / (a.e.wide ? 8 : 1);
     const int64_t blocks = (items + 255) / 256;
     hipLaunchKernelGGL(join_kernel, dim3(blocks < 1 << 20 ? blocks : 1 << 20), dim3(256), 0, s, a);
     return hipGetLastError();
