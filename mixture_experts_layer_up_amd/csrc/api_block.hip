@@ -84,7 +84,7 @@ struct ForwardLayout {
     size_t weight, partial, total;
     explicit ForwardLayout(const Sizes &z)
     {
-        rows = rows_kernel_takes(z.M, z.K, z.N, z.gated);
+        rows = rows_kernel_takes(z.M, z.N);
         plan = ProductPlan{};
         weight = partial = total = 0;
         if (z.M == 0 || rows)

@@ -56,13 +56,13 @@ struct ProductPlan {
 ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated);
 hipError_t launch_product(Product kind, const ProductPlan &plan, const ProductArgs &a, hipStream_t s);
 
-// The forward product for few rows: the weight as given, any N.
+// The forward product for few rows or few outputs: the weight as given, any N.
 struct RowsArgs {
     const uint16_t *x, *w;
     int M, K, W;
     Epilogue e;
 };
-bool rows_kernel_takes(int64_t M, int64_t K, int64_t N, bool gated);
+bool rows_kernel_takes(int64_t M, int64_t N);
 hipError_t launch_rows(const RowsArgs &a, hipStream_t s);
 
 // Copy of w [K, sets N] with each projection padded by zeros to `half` columns.

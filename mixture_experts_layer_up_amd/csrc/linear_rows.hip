@@ -1,7 +1,8 @@
-// linear_rows.hip -- the product with its epilogue for up to 64 rows, one launch:
+// linear_rows.hip -- the product with its epilogue for few rows or few outputs, one
+// launch:
 //   out[m, n] = epilogue(sum_k x[m, k] w[k, n])
-// Bound by the stream of w (and, below a few MB, by one launch and one chain of
-// loads), so w goes from memory straight into MFMA operands: a lane loads CPL
+// Bound by the stream of w (1 row of 4096 x 16384 weights: 21.5 us, 6.2 TB/s) or, below
+// a few MB, by one launch and one chain of loads (1 row of 2048 x 1536: 3.7 us), so w goes from memory straight into MFMA operands: a lane loads CPL
 // neighbouring columns of 8 terms, and one byte permutation per two weights makes
 // K-contiguous fragments of them, without LDS.  The 16 waves of a block split the
 // terms and are joined through LDS in a fixed order.  Any N: CPL divides it.
@@ -14,7 +15,7 @@ namespace {
 
 constexpr int kWaves = 16;
 
-// CPL columns (1, 2, 4 or 8 bf16) of one row of w as dwords
+// CPL columns (1, 2 or 4 bf16) of one row of w as dwords
 template <int CPL>
 struct Columns {
     static constexpr int kWords = CPL < 2 ? 1 : CPL / 2;
@@ -26,15 +27,10 @@ struct Columns {
             w[0] = *p;
         } else if constexpr (CPL == 2) {
             w[0] = *reinterpret_cast<const uint32_t *>(p);
-        } else if constexpr (CPL == 4) {
+        } else {
             const uint2 v = *reinterpret_cast<const uint2 *>(p);
             w[0] = v.x;
             w[1] = v.y;
-        } else {
-            const u32x4 v = load16(p);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = v[i];
         }
     }
     __device__ __forceinline__ void zero()
@@ -92,20 +88,23 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(RowsArgs a)
 {
     constexpr int kColumns = SETS * CPL * 16;     // sums of a row, set after set
     constexpr int kStride = kColumns + 4;         // rows of a column meet different banks
+    // chunks in flight: as many as leave a wave within its 128 registers
+    constexpr int kAhead = SETS * 8 * Columns<CPL>::kWords + 4 * MT <= 20 ? 4 : 2;
     __shared__ float part[kWaves][MT * 16][kStride];
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int i = lane & 15, g = lane >> 4;
-    const int blocks = (a.e.N + 16 * CPL - 1) / (16 * CPL);
-    const int item = xcd_balanced_item(blockIdx.x, blocks);
+    const int column_blocks = (a.e.N + 16 * CPL - 1) / (16 * CPL), row_blocks = (a.M + 16 * MT - 1) / (16 * MT);
+    const int item = xcd_balanced_item(blockIdx.x, column_blocks * row_blocks);
     if (item < 0)
         return;
-    const int n0 = item * 16 * CPL;
+    // the row blocks of one column block are neighbours: they share its columns of w
+    const int n0 = item / row_blocks * 16 * CPL, m0 = item % row_blocks * 16 * MT;
     const int c = n0 + i * CPL < a.e.N ? n0 + i * CPL : 0;   // N is a multiple of CPL
     const uint16_t *wp = a.w + c;
     const uint16_t *xp[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
-        xp[m] = a.x + (int64_t)(m * 16 + i < a.M ? m * 16 + i : a.M - 1) * a.K;
+        xp[m] = a.x + (int64_t)(m0 + m * 16 + i < a.M ? m0 + m * 16 + i : a.M - 1) * a.K;
 
     f32x4 acc[MT][SETS * CPL];
 #pragma unroll
@@ -124,15 +123,18 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(RowsArgs a)
                     acc[m][s * CPL + f] = mfma_16x16x32(fw, ch.x[m], acc[m][s * CPL + f]);
             }
     };
-    // chunks wave, wave + 16, ...; the next one's loads run under this one's products
+    // chunks wave, wave + 16, ...; past the last they are zeros
     const int chunks = (a.K + 31) / 32;
-    Chunk<MT, SETS, CPL> one, two;
-    one.load(xp, wp, a.e.N, a.W, wave * 32 + 8 * g, a.K);
-    for (int ch = wave; ch < chunks; ch += 2 * kWaves) {
-        two.load(xp, wp, a.e.N, a.W, (ch + kWaves) * 32 + 8 * g, a.K);
-        multiply(one);
-        one.load(xp, wp, a.e.N, a.W, (ch + 2 * kWaves) * 32 + 8 * g, a.K);
-        multiply(two);
+    Chunk<MT, SETS, CPL> ring[kAhead];
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d)
+        ring[d].load(xp, wp, a.e.N, a.W, (wave + d * kWaves) * 32 + 8 * g, a.K);
+    for (int ch = wave; ch < chunks; ch += kAhead * kWaves) {
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) {
+            multiply(ring[d]);
+            ring[d].load(xp, wp, a.e.N, a.W, (ch + (kAhead + d) * kWaves) * 32 + 8 * g, a.K);
+        }
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -147,7 +149,7 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(RowsArgs a)
     constexpr int kOut = MT * 16 * 16 * CPL;
     for (int e = threadIdx.x; e < kOut; e += kWaves * 64) {
         const int m = e / (16 * CPL), n = e % (16 * CPL);
-        if (m >= a.M || n0 + n >= a.e.N)
+        if (m0 + m >= a.M || n0 + n >= a.e.N)
             continue;
         float z = 0.0f, up = 0.0f;
 #pragma unroll
@@ -156,61 +158,61 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(RowsArgs a)
             if constexpr (SETS == 2)
                 up += part[w][m][16 * CPL + n];
         }
-        finish_one(a.e, m, n0 + n, z, up);
+        finish_one(a.e, m0 + m, n0 + n, z, up);
     }
 }
 
 template <int MT, int SETS, int CPL>
 hipError_t launch(const RowsArgs &a, hipStream_t s)
 {
-    const int blocks = (a.e.N + 16 * CPL - 1) / (16 * CPL);
+    const int blocks = ((a.e.N + 16 * CPL - 1) / (16 * CPL)) * ((a.M + 16 * MT - 1) / (16 * MT));
     hipLaunchKernelGGL((rows_kernel<MT, SETS, CPL>), dim3((blocks + 7) / 8 * 8), dim3(kWaves * 64), 0, s, a);
     return hipGetLastError();
 }
 
-// Columns a lane loads: the partial sums of 16 waves fit the LDS up to 8 / (MT SETS),
-// and N is a multiple; the fewest that leave at most 256 blocks.
-int columns_per_lane(int M, int N, int sets)
+// Sixteens of rows a block takes and columns a lane loads; mt = 0: not for this kernel.
+// Measured with 2048 terms, us: a block a CU takes 4 to 6, more blocks one another's
+// time again (64 rows, 4096 columns: (1, 2) 9.4, (2, 2) 7.2, tiles 9.2; 48 rows, 8192:
+// 14.3 and tiles 10.3; 128 rows, 1536: (2, 2) 7.1, tiles 8.6).  Fewer columns a lane give
+// small products more blocks (1 row, 128 columns: 3.5, two a lane 3.9), two make better
+// use of a line (16 rows, 4096 columns: 5.1 instead of 5.6).  Up to 16 rows w is read once
+// whatever the width: 4 columns a lane then stream it best (1 row, 4096 x 16384: 21.5,
+// two 25, eight 22.7).
+struct RowsPlan {
+    int mt, cpl;
+};
+
+RowsPlan plan_rows(int64_t M, int64_t N)
 {
-    const int mt = M <= 16 ? 1 : M <= 32 ? 2 : 4, most = 8 / (mt * sets);
-    int cpl = 1;
-    while (cpl < most && N % (2 * cpl) == 0 && (N + 16 * cpl - 1) / (16 * cpl) > 256)
-        cpl *= 2;
-    return cpl;
+    auto blocks = [&](int mt, int cpl) { return ((N + 16 * cpl - 1) / (16 * cpl)) * ((M + 16 * mt - 1) / (16 * mt)); };
+    const int cpl = N % 2 == 0 && blocks(1, 2) >= 96 ? 2 : 1;
+    if (blocks(1, cpl) <= 256)
+        return {1, cpl};
+    if (M <= 16)
+        return {1, N % 4 == 0 ? 4 : cpl};
+    if (blocks(2, cpl) <= 256)
+        return {2, cpl};
+    return {0, 0};
 }
 
-template <int MT, int SETS>
-hipError_t launch_columns(const RowsArgs &a, hipStream_t s)
+template <int SETS>
+hipError_t launch_sets(const RowsArgs &a, hipStream_t s)
 {
-    const int cpl = columns_per_lane(a.M, a.e.N, SETS);
-    if constexpr (8 / (MT * SETS) >= 8)
-        if (cpl == 8)
-            return launch<MT, SETS, 8>(a, s);
-    if constexpr (8 / (MT * SETS) >= 4)
-        if (cpl == 4)
-            return launch<MT, SETS, 4>(a, s);
-    if constexpr (8 / (MT * SETS) >= 2)
-        if (cpl == 2)
-            return launch<MT, SETS, 2>(a, s);
-    return launch<MT, SETS, 1>(a, s);
+    const RowsPlan p = plan_rows(a.M, a.e.N);
+    if (p.mt == 2)
+        return p.cpl == 2 ? launch<2, SETS, 2>(a, s) : launch<2, SETS, 1>(a, s);
+    return p.cpl == 4   ? launch<1, SETS, 4>(a, s)
+           : p.cpl == 2 ? launch<1, SETS, 2>(a, s)
+                        : launch<1, SETS, 1>(a, s);
 }
 
 } // namespace
 
-bool rows_kernel_takes(int64_t M, int64_t K, int64_t N, bool gated)
-{
-    (void)K, (void)N, (void)gated;
-    return M <= 64;
-}
+bool rows_kernel_takes(int64_t M, int64_t N) { return plan_rows(M, N).mt > 0; }
 
 hipError_t launch_rows(const RowsArgs &a, hipStream_t s)
 {
-    const bool gated = a.e.act == MOE_LORA_ACT_SWIGLU;
-    if (a.M <= 16)
-        return gated ? launch_columns<1, 2>(a, s) : launch_columns<1, 1>(a, s);
-    if (a.M <= 32)
-        return gated ? launch_columns<2, 2>(a, s) : launch_columns<2, 1>(a, s);
-    return gated ? launch_columns<4, 2>(a, s) : launch_columns<4, 1>(a, s);
+    return a.e.act == MOE_LORA_ACT_SWIGLU ? launch_sets<2>(a, s) : launch_sets<1>(a, s);
 }
 
 } // namespace moe_lora

@@ -259,18 +259,18 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void product_kernel(ProductArgs a)
         lds_order();
         const int first = m0 + wm * 16 + slab * kSlab;
         if (STORE >= kFull && !a.e.wide) {   // element by element, neighbours side by side
-#pragma unroll 1
+#pragma unroll 4
             for (int x = lane; x < kSlab * kOut; x += 64) {
                 const int r = x / kOut, o = x % kOut;
                 const float *from = turn + r * kTurn + (GATED ? (o >> 4) * 32 + (o & 15) : o);
                 finish_element(a.e, a.M, first + r, n0 + wn * (GATED ? 8 : 16) + o, from[0], GATED ? from[16] : 0.0f);
             }
         } else {
-#pragma unroll 1
+#pragma unroll 4
             for (int r = mine; r < kSlab; r += kAtOnce) {
                 const int64_t row = first + r;
                 if (row >= a.M || column >= (GATED ? a.e.half : a.C))
-                    break;
+                    continue;
                 const float *from = turn + r * kTurn + z_at;
                 float z[8], up[8];
 #pragma unroll

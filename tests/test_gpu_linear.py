@@ -54,13 +54,15 @@ def _forward(M, K, N, act, fp32=False, bias=True, residual=True, preact=True, se
 @pytest.mark.parametrize("act", _block.ACTS)
 @pytest.mark.parametrize("M,K,N", [(1, 64, 128), (3, 2048, 96), (16, 40, 17), (17, 72, 130), (33, 128, 36),
                                    (64, 1000, 8), (65, 64, 128), (100, 416, 1085), (129, 8, 1),
-                                   (256, 256, 256), (300, 328, 72)])
+                                   (256, 256, 256), (300, 328, 72), (700, 72, 545),
+                                   (1111, 64, 260), (4500, 136, 12), (6000, 8, 3)])
 def test_forward(M, K, N, act):
     _forward(M, K, N, act)
 
 
 @pytest.mark.parametrize("M,K,N,act", [(5, 2048, 60, "none"), (64, 2048, 128, "none"), (700, 2048, 128, "none"),
-                                       (129, 264, 33, "swiglu"), (1, 8, 1, "gelu")])
+                                       (129, 264, 33, "swiglu"), (1, 8, 1, "gelu"),
+                                       (900, 264, 333, "swiglu"), (3000, 72, 60, "silu")])
 def test_forward_fp32(M, K, N, act):
     _forward(M, K, N, act, fp32=True)
 
@@ -74,7 +76,7 @@ def test_forward_large(M, K, N, act):
     _forward(M, K, N, act, seed=2)
 
 
-@pytest.mark.parametrize("M,N", [(5, 96), (300, 96), (2048, 2048)])
+@pytest.mark.parametrize("M,N", [(5, 96), (300, 96), (2048, 100), (2048, 2048)])
 def test_residual_in_place(M, N):
     announce(f"linear residual in place {M} {N}")
     shape, x, w, b, res, _ = _make(M, 128, N, "none", 3)
@@ -84,7 +86,7 @@ def test_residual_in_place(M, N):
     assert _block.worst(res, want, bound) <= 1
 
 
-@pytest.mark.parametrize("M", [20, 200])
+@pytest.mark.parametrize("M", [20, 200, 1000])
 def test_unaligned_outputs(M):
     """Outputs, residual and bias one element off any boundary."""
     announce(f"linear unaligned {M}")
@@ -103,7 +105,7 @@ def test_unaligned_outputs(M):
 
 def test_non_finite_values_stay_in_their_rows_and_columns():
     """An infinity in a row of x or a column of w reaches no other row or column, also in tails."""
-    for M, K, N in ((20, 72, 100), (200, 72, 100), (300, 200, 300)):
+    for M, K, N in ((20, 72, 100), (200, 72, 100), (300, 200, 300), (2000, 72, 100), (2000, 200, 304)):
         announce(f"linear non-finite {M} {K} {N}")
         shape, x, w, _, _, _ = _make(M, K, N, "none", 5)
         want, bound, _, _ = _block.linear(x, w, "none")
@@ -119,7 +121,7 @@ def test_non_finite_values_stay_in_their_rows_and_columns():
 
 def test_neighbours_are_not_read_into_the_product():
     """NaN around x and w (the next rows of a larger buffer) never enters."""
-    for M, K, N in ((3, 40, 24), (70, 72, 40), (300, 136, 264)):
+    for M, K, N in ((3, 40, 24), (70, 72, 40), (300, 136, 264), (2100, 136, 265), (2100, 72, 1040)):
         announce(f"linear neighbours {M} {K} {N}")
         shape, x, w, _, _, _ = _make(M, K, N, "none", 6)
         bx = torch.full((M + 40, K), float("nan"), dtype=torch.bfloat16, device="cuda")
