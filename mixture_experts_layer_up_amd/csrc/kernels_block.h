@@ -52,6 +52,7 @@ enum class Product {
 struct ProductPlan {
     int tile;      // index of the tile shape
     int tiles_m, tiles_n, splits, k_per;
+    float us;      // estimate, without a launch's own time
 };
 ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated);
 hipError_t launch_product(Product kind, const ProductPlan &plan, const ProductArgs &a, hipStream_t s);
@@ -62,8 +63,12 @@ struct RowsArgs {
     int M, K, W;
     Epilogue e;
 };
-bool rows_kernel_takes(int64_t M, int64_t N);
-hipError_t launch_rows(const RowsArgs &a, hipStream_t s);
+struct RowsPlan {
+    int mt, cpl;   // sixteens of rows a block takes, columns a lane loads; mt 0: too large
+    float us;      // estimate
+};
+RowsPlan plan_rows(int64_t M, int64_t K, int64_t N);
+hipError_t launch_rows(const RowsPlan &plan, const RowsArgs &a, hipStream_t s);
 
 // Copy of w [K, sets N] with each projection padded by zeros to `half` columns.
 hipError_t launch_pad_columns(const uint16_t *w, uint16_t *out, int64_t K, int N, int half, int sets,

@@ -170,35 +170,18 @@ hipError_t launch(const RowsArgs &a, hipStream_t s)
     return hipGetLastError();
 }
 
-// Sixteens of rows a block takes and columns a lane loads; mt = 0: not for this kernel.
-// Measured with 2048 terms, us: a block a CU takes 4 to 6, more blocks one another's
-// time again (64 rows, 4096 columns: (1, 2) 9.4, (2, 2) 7.2, tiles 9.2; 48 rows, 8192:
-// 14.3 and tiles 10.3; 128 rows, 1536: (2, 2) 7.1, tiles 8.6).  Fewer columns a lane give
-// small products more blocks (1 row, 128 columns: 3.5, two a lane 3.9), two make better
-// use of a line (16 rows, 4096 columns: 5.1 instead of 5.6).  Up to 16 rows w is read once
-// whatever the width: 4 columns a lane then stream it best (1 row, 4096 x 16384: 21.5,
-// two 25, eight 22.7).
-struct RowsPlan {
+// Microseconds of a block on a CU that runs others too: its reduction and epilogue,
+// and its terms.  Fitted to 64 to 1000 rows, 64 to 2048 terms and 128 to 4096 columns
+// within a fifth; a chip with fewer blocks than CUs is up to twice as fast.
+struct Body {
     int mt, cpl;
+    float fixed, term;
 };
-
-RowsPlan plan_rows(int64_t M, int64_t N)
-{
-    auto blocks = [&](int mt, int cpl) { return ((N + 16 * cpl - 1) / (16 * cpl)) * ((M + 16 * mt - 1) / (16 * mt)); };
-    const int cpl = N % 2 == 0 && blocks(1, 2) >= 96 ? 2 : 1;
-    if (blocks(1, cpl) <= 256)
-        return {1, cpl};
-    if (M <= 16)
-        return {1, N % 4 == 0 ? 4 : cpl};
-    if (blocks(2, cpl) <= 256)
-        return {2, cpl};
-    return {0, 0};
-}
+constexpr Body kBodies[] = {{1, 1, 0.8f, 0.0017f}, {1, 2, 1.0f, 0.0014f}, {2, 1, 1.2f, 0.0026f}, {2, 2, 1.3f, 0.0019f}};
 
 template <int SETS>
-hipError_t launch_sets(const RowsArgs &a, hipStream_t s)
+hipError_t launch_sets(const RowsPlan &p, const RowsArgs &a, hipStream_t s)
 {
-    const RowsPlan p = plan_rows(a.M, a.e.N);
     if (p.mt == 2)
         return p.cpl == 2 ? launch<2, SETS, 2>(a, s) : launch<2, SETS, 1>(a, s);
     return p.cpl == 4   ? launch<1, SETS, 4>(a, s)
@@ -208,11 +191,30 @@ hipError_t launch_sets(const RowsArgs &a, hipStream_t s)
 
 } // namespace
 
-bool rows_kernel_takes(int64_t M, int64_t N) { return plan_rows(M, N).mt > 0; }
-
-hipError_t launch_rows(const RowsArgs &a, hipStream_t s)
+// Up to 16 rows w is read once whatever the width: 4 columns a lane then stream it best
+// (1 row, 4096 x 16384: 21.5 us, two columns 25).  For few blocks one column a lane is
+// best, which gives twice as many (32 rows, 2048 x 60: 4.7, two 7.2).
+RowsPlan plan_rows(int64_t M, int64_t K, int64_t N)
 {
-    return a.e.act == MOE_LORA_ACT_SWIGLU ? launch_sets<2>(a, s) : launch_sets<1>(a, s);
+    RowsPlan best{0, 0, 0.0f};
+    for (const Body &b : kBodies) {
+        if (N % b.cpl != 0 || (b.mt > 1 && M <= 16))
+            continue;
+        const int64_t blocks = ((N + 16 * b.cpl - 1) / (16 * b.cpl)) * ((M + 16 * b.mt - 1) / (16 * b.mt));
+        const float us = 2.0f + (float)((blocks + 255) / 256) * (b.fixed + b.term * K);
+        if (blocks < 1 << 20 && (best.mt == 0 || us < best.us))
+            best = {b.mt, b.cpl, us};
+        if (b.mt == 1 && b.cpl == 1 && blocks <= 128)
+            return best;
+    }
+    if (M <= 16 && N % 4 == 0 && N > 16 * 2 * 256)
+        best = {1, 4, 0.0f};
+    return best;
+}
+
+hipError_t launch_rows(const RowsPlan &plan, const RowsArgs &a, hipStream_t s)
+{
+    return a.e.act == MOE_LORA_ACT_SWIGLU ? launch_sets<2>(plan, a, s) : launch_sets<1>(plan, a, s);
 }
 
 } // namespace moe_lora

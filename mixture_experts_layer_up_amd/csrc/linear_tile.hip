@@ -395,7 +395,6 @@ ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated)
 {
     const int64_t steps = (K + BK - 1) / BK;
     ProductPlan best{};
-    float least = 0.0f;
     for (int t = 0; t < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++t) {
         const Tile &tile = kTiles[t];
         const int64_t tiles = ((M + tile.rows - 1) / tile.rows) * ((C + tile.columns - 1) / tile.columns);
@@ -411,8 +410,8 @@ ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated)
             float us = per * (each == 1 ? tile.alone : each * tile.shared);
             if (splits > 1)
                 us += 3.0f + (float)splits * M * C * 8.0f / 5e6f;
-            if (best.tiles_m == 0 || us < least) {
-                least = us;
+            if (best.tiles_m == 0 || us < best.us) {
+                best.us = us;
                 best.tile = t;
                 best.splits = (int)((steps + per - 1) / per);
                 best.k_per = (int)(per * BK);

@@ -79,7 +79,7 @@ def test_bad_linear_shapes(lib, over, rc):
 
 
 def test_linear_arguments(lib):
-    s = _linear_shape(rows=3000, out_features=49)     # needs a workspace: a padded weight
+    s = _linear_shape(rows=60000, out_features=49)    # needs a workspace: a padded weight
     assert _linear(lib, None) == INVALID and _linear_grad(lib, None) == INVALID
     for name in ("x", "w", "out", "ws"):
         assert _linear(lib, s, **{name: None}) == INVALID
