@@ -8,7 +8,9 @@ implementation to fall back to.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import itertools
 import os
 import re
 from typing import Dict, Optional, Sequence
@@ -700,16 +702,48 @@ def _scratch(need: int, device) -> Optional[torch.Tensor]:
     return torch.empty(need, dtype=torch.uint8, device=device) if need else None
 
 
+def _given(t: Optional[torch.Tensor], dtype, shape, name: str):
+    """:func:`_ptr` of a tensor whose device is known, the checks of a good call first: the
+    smallest kernels take as long as these."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    return _ptr(t, _BF16 if dtype is torch.bfloat16 else dtype, shape, name)
+
+
+def _workspace(t: Optional[torch.Tensor]):
+    """(pointer, bytes) of a workspace tensor."""
+    if t is None:
+        return None, 0
+    return _ptr(t, None, None, "workspace"), t.numel() * t.element_size()
+
+
+def _run(index: int, call, *args):
+    """call(*args, current stream of GPU `index`) with that GPU current, and its status."""
+    if index == torch._C._cuda_getDevice():
+        rc = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        _check(rc)
+
+
+_bf16, _fp32 = torch.bfloat16, torch.float32
+
+
+def _rows_like(some: torch.Tensor, rows) -> torch.Tensor:
+    """A new bf16 tensor of `rows`, the shape of `some`."""
+    return torch.empty_like(some) if some.dtype is _bf16 else some.new_empty(rows, dtype=_bf16)
+
+
 def linear_workspace_size(shape: LinearShape) -> int:
     return int(load_library().moe_lora_linear_workspace_size(ctypes.byref(shape)))
 
 
 def linear_backward_workspace_size(shape: LinearShape) -> int:
     return int(load_library().moe_lora_linear_backward_workspace_size(ctypes.byref(shape)))
-
-
-def _weight_columns(shape: LinearShape) -> int:
-    return 2 * shape.out_features if shape.activation == 4 else shape.out_features
 
 
 def linear(shape: LinearShape, x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -721,20 +755,18 @@ def linear(shape: LinearShape, x: torch.Tensor, w: torch.Tensor, bias: Optional[
     ``x`` bf16 [M, K]; ``w`` bf16 [K, W] with W = N, for swiglu 2N (gate columns, then
     up columns); ``bias`` fp32 [W]; ``residual`` bf16 [M, N], which ``out`` may be.
     ``preact`` (bf16 [M, W]) receives x w + bias for :func:`linear_backward`."""
-    M, K, N, W = shape.rows, shape.in_features, shape.out_features, _weight_columns(shape)
+    M, K, N = shape.rows, shape.in_features, shape.out_features
+    W = 2 * N if shape.activation == 4 else N
     gpu = _one_gpu(x, w, bias, residual, out, preact, workspace)
-    kind = torch.float32 if shape.out_fp32 else torch.bfloat16
+    kind = _fp32 if shape.out_fp32 else _bf16
     if out is None:
-        out = torch.empty((M, N), dtype=kind, device=x.device)
-    lib = load_library()
+        out = x.new_empty((M, N), dtype=kind)
+    lib, ref = load_library(), ctypes.byref(shape)
     if workspace is None:
-        workspace = _scratch(lib.moe_lora_linear_workspace_size(ctypes.byref(shape)), x.device)
-    args = (ctypes.byref(shape), _ptr(x, _BF16, (M, K), "x"), _ptr(w, _BF16, (K, W), "w"),
-            _ptr(bias, torch.float32, (W,), "bias"), _ptr(residual, _BF16, (M, N), "residual"),
-            _ptr(out, kind if shape.out_fp32 else _BF16, (M, N), "out"),
-            _ptr(preact, _BF16, (M, W), "preact"), _ptr(workspace, None, None, "workspace"),
-            workspace.numel() * workspace.element_size() if workspace is not None else 0)
-    _check(_on(gpu, lambda stream: lib.moe_lora_linear(*args, stream)))
+        workspace = _scratch(lib.moe_lora_linear_workspace_size(ref), x.device)
+    _run(gpu, lib.moe_lora_linear, ref, _given(x, _bf16, (M, K), "x"), _given(w, _bf16, (K, W), "w"),
+         _given(bias, _fp32, (W,), "bias"), _given(residual, _bf16, (M, N), "residual"),
+         _given(out, kind, (M, N), "out"), _given(preact, _bf16, (M, W), "preact"), *_workspace(workspace))
     return out
 
 
@@ -748,39 +780,30 @@ def linear_backward(shape: LinearShape, x: Optional[torch.Tensor], w: Optional[t
     bf16 [M, K], ``d_w`` bf16 [K, W], ``d_bias`` fp32 [W], None for those not asked
     for.  ``preact`` as the forward wrote it (None without an activation); the
     residual's gradient is ``d_out`` itself.  ``d_x`` may be ``x``."""
-    M, K, N, W = shape.rows, shape.in_features, shape.out_features, _weight_columns(shape)
+    M, K, N = shape.rows, shape.in_features, shape.out_features
+    W = 2 * N if shape.activation == 4 else N
     gpu = _one_gpu(d_out, x, w, preact, d_x, d_w, d_bias, workspace)
-    dev = d_out.device
     if not x_grad:
         d_x = None
     elif d_x is None:
-        d_x = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        d_x = d_out.new_empty((M, K), dtype=_bf16)
     if not w_grad:
         d_w = None
     elif d_w is None:
-        d_w = torch.empty((K, W), dtype=torch.bfloat16, device=dev)
+        d_w = d_out.new_empty((K, W), dtype=_bf16)
     if not bias_grad:
         d_bias = None
     elif d_bias is None:
-        d_bias = torch.empty(W, dtype=torch.float32, device=dev)
-    lib = load_library()
+        d_bias = d_out.new_empty(W, dtype=_fp32)
+    lib, ref = load_library(), ctypes.byref(shape)
     if workspace is None:
-        workspace = _scratch(lib.moe_lora_linear_backward_workspace_size(ctypes.byref(shape)), dev)
-    args = (ctypes.byref(shape), _ptr(x, _BF16, (M, K), "x"), _ptr(w, _BF16, (K, W), "w"),
-            _ptr(preact, _BF16, (M, W), "preact"),
-            _ptr(d_out, torch.float32 if shape.out_fp32 else _BF16, (M, N), "d_out"),
-            _ptr(d_x, _BF16, (M, K), "d_x"), _ptr(d_w, _BF16, (K, W), "d_w"),
-            _ptr(d_bias, torch.float32, (W,), "d_bias"), _ptr(workspace, None, None, "workspace"),
-            workspace.numel() * workspace.element_size() if workspace is not None else 0)
-    _check(_on(gpu, lambda stream: lib.moe_lora_linear_backward(*args, stream)))
+        workspace = _scratch(lib.moe_lora_linear_backward_workspace_size(ref), d_out.device)
+    _run(gpu, lib.moe_lora_linear_backward, ref, _given(x, _bf16, (M, K), "x"),
+         _given(w, _bf16, (K, W), "w"), _given(preact, _bf16, (M, W), "preact"),
+         _given(d_out, _fp32 if shape.out_fp32 else _bf16, (M, N), "d_out"),
+         _given(d_x, _bf16, (M, K), "d_x"), _given(d_w, _bf16, (K, W), "d_w"),
+         _given(d_bias, _fp32, (W,), "d_bias"), *_workspace(workspace))
     return {"d_x": d_x, "d_w": d_w, "d_bias": d_bias}
-
-
-def _gate_arguments(shape: NormShape):
-    """Type and shape of the gate."""
-    if shape.gate == 1:
-        return torch.float32, (shape.rows,)
-    return _BF16, (shape.hidden,)
 
 
 def block_norm(shape: NormShape, residual: Optional[torch.Tensor], branch: Optional[torch.Tensor],
@@ -795,23 +818,24 @@ def block_norm(shape: NormShape, residual: Optional[torch.Tensor], branch: Optio
     bf16 [H]; ``gate`` fp32 [T] or bf16 [H] as ``shape.gate`` says.  ``residual`` or
     ``branch`` may be None (0), and either may be an output.  With ``residual_out``
     False only ``normed`` is written."""
-    T, H = shape.rows, shape.hidden
     some = residual if residual is not None else branch
     if some is None:
         raise MoELoRAError("residual or branch must be given")
+    H = shape.hidden
+    rows, col = (shape.rows, H), (H,)
     gpu = _one_gpu(residual, branch, post_weight, pre_weight, gate, new_residual, normed)
     if not residual_out:
         new_residual = None
     elif new_residual is None:
-        new_residual = torch.empty((T, H), dtype=torch.bfloat16, device=some.device)
+        new_residual = _rows_like(some, rows)
     if normed is None and pre_weight is not None:
-        normed = torch.empty((T, H), dtype=torch.bfloat16, device=some.device)
-    rows, col = (T, H), (H,)
-    args = (ctypes.byref(shape), _ptr(residual, _BF16, rows, "residual"), _ptr(branch, _BF16, rows, "branch"),
-            _ptr(post_weight, _BF16, col, "post_weight"), _ptr(pre_weight, _BF16, col, "pre_weight"),
-            _ptr(gate, *_gate_arguments(shape), "gate"), _ptr(new_residual, _BF16, rows, "new_residual"),
-            _ptr(normed, _BF16, rows, "normed"))
-    _check(_on(gpu, lambda stream: load_library().moe_lora_block_norm(*args, stream)))
+        normed = _rows_like(some, rows)
+    token = shape.gate == 1
+    _run(gpu, load_library().moe_lora_block_norm, ctypes.byref(shape),
+         _given(residual, _bf16, rows, "residual"), _given(branch, _bf16, rows, "branch"),
+         _given(post_weight, _bf16, col, "post_weight"), _given(pre_weight, _bf16, col, "pre_weight"),
+         _given(gate, _fp32 if token else _bf16, (shape.rows,) if token else col, "gate"),
+         _given(new_residual, _bf16, rows, "new_residual"), _given(normed, _bf16, rows, "normed"))
     return new_residual, normed
 
 
@@ -830,57 +854,75 @@ def block_norm_backward(shape: NormShape, new_residual: Optional[torch.Tensor],
     ``d_normed`` (bf16 [T, H], None: 0), at ``new_residual`` as it wrote it: a dict of
     ``residual`` and ``branch`` (bf16 [T, H]), ``post_weight``, ``pre_weight`` and
     ``gate`` (fp32), None for what is not in ``wanted`` or has no input.  ``out`` may
-    hold tensors to write them to."""
-    T, H = shape.rows, shape.hidden
-    out = dict(out) if out else {}
+    hold tensors to write them to; new [H] gradients share one buffer."""
     some = d_residual if d_residual is not None else d_normed
     if some is None:
         raise MoELoRAError("d_residual or d_normed must be given")
+    H = shape.hidden
+    rows, col = (shape.rows, H), (H,)
+    out = out or {}
     gpu = _one_gpu(new_residual, branch, post_weight, pre_weight, gate, d_residual, d_normed, workspace,
                    *out.values())
-    has = {"residual": True, "branch": branch is not None, "post_weight": post_weight is not None,
-           "pre_weight": pre_weight is not None and d_normed is not None, "gate": gate is not None}
-    rows, col = (T, H), (H,)
-    sizes = {"residual": rows, "branch": rows, "post_weight": col, "pre_weight": col,
-             "gate": (T,) if shape.gate == 1 else col}
-    got, ptrs = {}, []
-    for name, size in sizes.items():
-        if name not in wanted or not has[name]:
-            got[name] = None
-            ptrs.append(None)
-            continue
-        kind = torch.bfloat16 if size is rows else torch.float32
-        t = out.get(name)
-        if t is None:
-            t = torch.empty(size, dtype=kind, device=some.device)
-        got[name] = t
-        ptrs.append(_ptr(t, _BF16 if size is rows else kind, size, name + " gradient"))
-    lib = load_library()
+    token = shape.gate == 1
+    got = dict.fromkeys(("residual", "branch", "post_weight", "pre_weight", "gate"))
+    columns = []      # fp32 [H] gradients without a tensor
+    for name, there in (("residual", True), ("branch", branch is not None),
+                        ("post_weight", post_weight is not None),
+                        ("pre_weight", pre_weight is not None and d_normed is not None),
+                        ("gate", gate is not None)):
+        if there and name in wanted:
+            t = out.get(name)
+            if t is None:
+                if name in ("residual", "branch"):
+                    t = _rows_like(some, rows)
+                elif name == "gate" and token:
+                    t = some.new_empty(shape.rows, dtype=_fp32)
+                else:
+                    columns.append(name)
+            got[name] = t
+    if columns:
+        got.update(zip(columns, some.new_empty((len(columns), H), dtype=_fp32).unbind(0)))
+    gate_shape = (shape.rows,) if token else col
+    gradients = NormGradients(
+        _given(got["residual"], _bf16, rows, "residual gradient"),
+        _given(got["branch"], _bf16, rows, "branch gradient"),
+        _given(got["post_weight"], _fp32, col, "post_weight gradient"),
+        _given(got["pre_weight"], _fp32, col, "pre_weight gradient"),
+        _given(got["gate"], _fp32, gate_shape, "gate gradient"))
+    lib, ref = load_library(), ctypes.byref(shape)
     if workspace is None:
-        workspace = _scratch(lib.moe_lora_block_norm_backward_workspace_size(ctypes.byref(shape)), some.device)
-    args = (ctypes.byref(shape), _ptr(new_residual, _BF16, rows, "new_residual"),
-            _ptr(branch, _BF16, rows, "branch"), _ptr(post_weight, _BF16, col, "post_weight"),
-            _ptr(pre_weight, _BF16, col, "pre_weight"), _ptr(gate, *_gate_arguments(shape), "gate"),
-            _ptr(d_residual, _BF16, rows, "d_residual"), _ptr(d_normed, _BF16, rows, "d_normed"),
-            ctypes.byref(NormGradients(*ptrs)), _ptr(workspace, None, None, "workspace"),
-            workspace.numel() * workspace.element_size() if workspace is not None else 0)
-    _check(_on(gpu, lambda stream: lib.moe_lora_block_norm_backward(*args, stream)))
+        workspace = _scratch(lib.moe_lora_block_norm_backward_workspace_size(ref), some.device)
+    _run(gpu, lib.moe_lora_block_norm_backward, ref, _given(new_residual, _bf16, rows, "new_residual"),
+         _given(branch, _bf16, rows, "branch"), _given(post_weight, _bf16, col, "post_weight"),
+         _given(pre_weight, _bf16, col, "pre_weight"),
+         _given(gate, _fp32 if token else _bf16, gate_shape, "gate"),
+         _given(d_residual, _bf16, rows, "d_residual"), _given(d_normed, _bf16, rows, "d_normed"),
+         ctypes.byref(gradients), *_workspace(workspace))
     return got
 
 
 def _gradients(gradients: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]]):
-    """The moe_lora_gradient array of the tensors."""
-    if out is None:
-        out = gradients
-    elif len(out) != len(gradients):
-        raise MoELoRAError(f"out has {len(out)} tensors, gradients has {len(gradients)}")
-    table = (Gradient * len(gradients))()
-    for entry, g, o in zip(table, gradients, out):
-        entry.data = data = _ptr(g, (torch.bfloat16, torch.float32), None, "gradient")
-        entry.out = data if o is g else _ptr(o, g.dtype, g.shape, "out")
-        entry.elements = g.numel()
-        entry.fp32 = g.dtype is torch.float32
-    return table
+    """The moe_lora_gradient array of the tensors: four 64-bit words each.  Attribute by
+    attribute over all tensors: one by one with their own checks, 60 tensors cost more
+    than their kernels."""
+    def row(tensors):
+        return [t.dtype for t in tensors], [t.numel() for t in tensors], [t.data_ptr() for t in tensors]
+
+    kinds, sizes, at = row(gradients)
+    if not {_fp32, _bf16}.issuperset(kinds) or not all([t.is_contiguous() for t in gradients]):
+        for g in gradients:
+            _ptr(g, (_bf16, _fp32), None, "gradient")
+    to = at
+    if out is not None:
+        if len(out) != len(gradients):
+            raise MoELoRAError(f"out has {len(out)} tensors, gradients has {len(gradients)}")
+        out_kinds, out_sizes, to = row(out)
+        if out_kinds != kinds or out_sizes != sizes or not all([t.is_contiguous() for t in out]):
+            for g, o in zip(gradients, out):
+                _ptr(o, g.dtype, g.shape, "out")
+    words = array.array("q", itertools.chain.from_iterable(
+        zip(at, to, sizes, [kind is _fp32 for kind in kinds])))
+    return (Gradient * len(gradients)).from_buffer(words)
 
 
 def clip_workspace_size(gradients: Sequence[torch.Tensor]) -> int:
@@ -894,19 +936,18 @@ def clip_gradients(gradients: Sequence[torch.Tensor], max_norm: float,
     global norm, in place or into ``out``: (``norm`` fp32 [1], the scaled tensors).
     A norm that is not finite leaves the values as they are; ``max_norm`` = inf only
     takes the norm."""
-    if not len(gradients):
+    n = len(gradients)
+    if not n:
         raise MoELoRAError("no gradients given")
     gpu = _one_gpu(*gradients, *(out if out is not None else ()), norm, workspace)
-    dev = gradients[0].device
     table = _gradients(gradients, out)
     if norm is None:
-        norm = torch.empty(1, dtype=torch.float32, device=dev)
+        norm = gradients[0].new_empty(1, dtype=_fp32)
     lib = load_library()
     if workspace is None:
-        workspace = _scratch(lib.moe_lora_clip_workspace_size(table, len(table)), dev)
-    args = (table, len(table), max_norm, _ptr(norm, torch.float32, (1,), "norm"),
-            _ptr(workspace, None, None, "workspace"), workspace.numel() * workspace.element_size())
-    _check(_on(gpu, lambda stream: lib.moe_lora_clip_gradients(*args, stream)))
+        workspace = _scratch(lib.moe_lora_clip_workspace_size(table, n), gradients[0].device)
+    _run(gpu, lib.moe_lora_clip_gradients, table, n, max_norm, _given(norm, _fp32, (1,), "norm"),
+         *_workspace(workspace))
     return norm, list(out if out is not None else gradients)
 
 

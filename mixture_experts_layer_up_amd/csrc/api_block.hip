@@ -162,13 +162,23 @@ constexpr int kMostTensors = 4096;
 constexpr int64_t kMostElements = (int64_t)1 << 36;
 constexpr int64_t kMostBlocks = 1 << 23;   // of a launch: its threads stay below 2^32
 
-int64_t chunks_of(const moe_lora_gradient &g) { return (g.elements + kClipChunk - 1) / kClipChunk; }
-
-int64_t total_chunks(const moe_lora_gradient *g, int32_t count)
+// Elements of a block: few values are spread over more blocks.
+int chunk_of(const moe_lora_gradient *g, int32_t count)
 {
     int64_t n = 0;
     for (int32_t i = 0; i < count; ++i)
-        n += chunks_of(g[i]);
+        n += g[i].elements;
+    int chunk = 2048;
+    while (chunk < 32768 && n > chunk * (int64_t)1024)
+        chunk *= 2;
+    return chunk;
+}
+
+int64_t total_chunks(const moe_lora_gradient *g, int32_t count, int chunk)
+{
+    int64_t n = 0;
+    for (int32_t i = 0; i < count; ++i)
+        n += (g[i].elements + chunk - 1) / chunk;
     return n;
 }
 
@@ -207,13 +217,14 @@ bool ranges_apart(Range *r, int n)
 // f(table, first chunk of the table) over the tensors with elements, as many to a
 // table as fit
 template <class F>
-int for_tables(const moe_lora_gradient *g, int32_t count, F f)
+int for_tables(const moe_lora_gradient *g, int32_t count, int chunk, F f)
 {
     ClipTable t;
+    t.chunk = chunk;
     t.count = t.blocks = 0;
     int64_t done = 0;
     for (int32_t i = 0; i <= count; ++i) {
-        const int64_t chunks = i < count ? chunks_of(g[i]) : 0;
+        const int64_t chunks = i < count ? (g[i].elements + chunk - 1) / chunk : 0;
         if (t.count > 0 && (i == count || t.count == kClipTensors || t.blocks + chunks > kMostBlocks)) {
             const hipError_t rc = f(t, done);
             if (rc != hipSuccess)
@@ -400,7 +411,8 @@ size_t moe_lora_block_norm_backward_workspace_size(const moe_lora_norm_shape *sh
 {
     if (validate(shape) != MOE_LORA_OK)
         return 0;
-    return align_up((size_t)norm_grad_blocks(shape->rows, shape->hidden) * 3 * shape->hidden * sizeof(float));
+    return align_up(norm_grad_stats_bytes(shape->rows, shape->hidden)) +
+           align_up((size_t)norm_grad_blocks(shape->rows, shape->hidden) * 3 * shape->hidden * sizeof(float));
 }
 
 int moe_lora_block_norm_backward(const moe_lora_norm_shape *shape, const void *new_residual,
@@ -446,7 +458,9 @@ int moe_lora_block_norm_backward(const moe_lora_norm_shape *shape, const void *n
     a.dz = static_cast<const uint16_t *>(d_normed);
     a.dx = static_cast<uint16_t *>(d.d_residual);
     a.dy = static_cast<uint16_t *>(d.d_branch);
-    a.partial = static_cast<float *>(workspace);
+    a.stats = static_cast<float4 *>(workspace);
+    a.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                          align_up(norm_grad_stats_bytes(shape->rows, shape->hidden)));
     float *to[3];
     auto place = [&](float *out) {
         if (!out)
@@ -473,7 +487,7 @@ size_t moe_lora_clip_workspace_size(const moe_lora_gradient *gradients, int32_t 
 {
     if (validate(gradients, count) != MOE_LORA_OK)
         return 0;
-    return kAlign + align_up((size_t)total_chunks(gradients, count) * sizeof(double));
+    return kAlign + align_up((size_t)total_chunks(gradients, count, chunk_of(gradients, count)) * sizeof(double));
 }
 
 int moe_lora_clip_gradients(const moe_lora_gradient *gradients, int32_t count, float max_norm,
@@ -505,16 +519,19 @@ int moe_lora_clip_gradients(const moe_lora_gradient *gradients, int32_t count, f
         return MOE_LORA_ERR_INVALID_ARG;
     MOE_TRY(check_workspace(workspace, workspace_bytes, moe_lora_clip_workspace_size(gradients, count)));
     hipStream_t st = static_cast<hipStream_t>(stream);
-    float *factor = static_cast<float *>(workspace);
-    double *partial = reinterpret_cast<double *>(static_cast<char *>(workspace) + kAlign);
-    MOE_TRY(for_tables(gradients, count, [&](const ClipTable &t, int64_t done) {
-        return launch_clip_squares(t, partial + done, st);
+    const int chunk = chunk_of(gradients, count);
+    const ClipSums c{reinterpret_cast<double *>(static_cast<char *>(workspace) + kAlign),
+                     total_chunks(gradients, count, chunk), norm, static_cast<float *>(workspace), max_norm};
+    MOE_TRY(for_tables(gradients, count, chunk, [&](const ClipTable &t, int64_t done) {
+        return launch_clip_squares(t, c.partial + done, st);
     }));
-    MOE_TRY(check(launch_clip_norm(partial, total_chunks(gradients, count), max_norm, norm, factor, st)));
+    if (!scales || c.blocks == 0 || c.blocks > kClipFew)
+        MOE_TRY(check(launch_clip_norm(c, st)));
     if (!scales)
         return MOE_LORA_OK;
-    return for_tables(gradients, count,
-                      [&](const ClipTable &t, int64_t) { return launch_clip_scale(t, factor, st); });
+    return for_tables(gradients, count, chunk, [&](const ClipTable &t, int64_t done) {
+        return launch_clip_scale(t, c, done == 0, st);
+    });
 }
 
 } // extern "C"

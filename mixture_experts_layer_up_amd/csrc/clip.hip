@@ -150,9 +150,9 @@ __global__ __launch_bounds__(kThreads) void clip_squares_kernel(ClipTable t, dou
 {
     __shared__ double part[kThreads / kWave];
     const int i = find_tensor(t, blockIdx.x);
-    const int64_t at = (int64_t)((int)blockIdx.x - t.t[i].first) * kClipChunk;
+    const int64_t at = (int64_t)((int)blockIdx.x - t.t[i].first) * t.chunk;
     const int64_t left = t.t[i].n - at;
-    const int n = left < kClipChunk ? (int)left : kClipChunk;
+    const int n = left < t.chunk ? (int)left : t.chunk;
     double s = t.t[i].fp32 ? chunk_squares<1>(t.t[i].data, at, n) : chunk_squares<0>(t.t[i].data, at, n);
     s = wave_sum(s);
     if ((threadIdx.x & (kWave - 1)) == 0)
@@ -165,45 +165,67 @@ __global__ __launch_bounds__(kThreads) void clip_squares_kernel(ClipTable t, dou
     }
 }
 
-constexpr int kNormThreads = 1024;
-
-__global__ __launch_bounds__(kNormThreads) void clip_norm_kernel(const double *partial, int64_t blocks,
-                                                                 float max_norm, float *norm, float *factor)
+// Sum of all partial sums by THREADS threads, the same bits in every block, and the norm
+// and the factor that come of it.
+template <int THREADS>
+__device__ __forceinline__ float factor_of(const ClipSums &c, float *norm)
 {
-    __shared__ double part[kNormThreads / kWave];
+    __shared__ double part[THREADS / kWave];
     double s = 0.0;
 #pragma unroll 4
-    for (int64_t b = threadIdx.x; b < blocks; b += kNormThreads)
-        s += partial[b];
+    for (int64_t b = threadIdx.x; b < c.blocks; b += THREADS)
+        s += c.partial[b];
     s = wave_sum(s);
     if ((threadIdx.x & (kWave - 1)) == 0)
         part[wave_id()] = s;
     __syncthreads();
-    if (threadIdx.x != 0)
-        return;
-    for (int w = 1; w < kNormThreads / kWave; ++w)
+    s = 0.0;
+#pragma unroll
+    for (int w = 0; w < THREADS / kWave; ++w)
         s += part[w];
     const double total = sqrt(s);
-    const float rounded = (float)total;
-    *norm = rounded;
+    *norm = (float)total;
     // a norm that is not finite (as the caller sees it): leave the values as they are
-    const double c = (double)max_norm / (total + 1e-6);
-    *factor = rounded < __builtin_inff() && c < 1.0 ? (float)c : 1.0f;
+    const double f = (double)c.max_norm / (total + 1e-6);
+    return *norm < __builtin_inff() && f < 1.0 ? (float)f : 1.0f;
 }
 
-__global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable t, const float *factor)
+constexpr int kNormThreads = 1024;
+
+__global__ __launch_bounds__(kNormThreads) void clip_norm_kernel(ClipSums c)
 {
-    const float c = *factor;
+    float norm;
+    const float f = factor_of<kNormThreads>(c, &norm);
+    if (threadIdx.x == 0) {
+        *c.norm = norm;
+        *c.factor = f;
+    }
+}
+
+// FEW: the blocks sum the partial sums themselves (up to 4096, 32 KB from the cache) and
+// save a launch: 5 tensors of 0.3 M elements 14.3 -> @@ us in kernels.
+template <bool FEW>
+__global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable t, ClipSums c, int first_table)
+{
+    float f;
+    if constexpr (FEW) {
+        float norm;
+        f = factor_of<kThreads>(c, &norm);
+        if (first_table && blockIdx.x == 0 && threadIdx.x == 0)
+            *c.norm = norm;
+    } else {
+        f = *c.factor;
+    }
     const int i = find_tensor(t, blockIdx.x);
-    if (c == 1.0f && t.t[i].out == t.t[i].data)
+    if (f == 1.0f && t.t[i].out == t.t[i].data)
         return;
-    const int64_t at = (int64_t)((int)blockIdx.x - t.t[i].first) * kClipChunk;
+    const int64_t at = (int64_t)((int)blockIdx.x - t.t[i].first) * t.chunk;
     const int64_t left = t.t[i].n - at;
-    const int n = left < kClipChunk ? (int)left : kClipChunk;
+    const int n = left < t.chunk ? (int)left : t.chunk;
     if (t.t[i].fp32)
-        chunk_scale<1>(t.t[i].data, t.t[i].out, at, n, c);
+        chunk_scale<1>(t.t[i].data, t.t[i].out, at, n, f);
     else
-        chunk_scale<0>(t.t[i].data, t.t[i].out, at, n, c);
+        chunk_scale<0>(t.t[i].data, t.t[i].out, at, n, f);
 }
 
 } // namespace
@@ -214,17 +236,18 @@ hipError_t launch_clip_squares(const ClipTable &t, double *partial, hipStream_t 
     return hipGetLastError();
 }
 
-hipError_t launch_clip_norm(const double *partial, int64_t blocks, float max_norm, float *norm,
-                            float *factor, hipStream_t s)
+hipError_t launch_clip_norm(const ClipSums &c, hipStream_t s)
 {
-    hipLaunchKernelGGL(clip_norm_kernel, dim3(1), dim3(kNormThreads), 0, s, partial, blocks, max_norm, norm,
-                       factor);
+    hipLaunchKernelGGL(clip_norm_kernel, dim3(1), dim3(kNormThreads), 0, s, c);
     return hipGetLastError();
 }
 
-hipError_t launch_clip_scale(const ClipTable &t, const float *factor, hipStream_t s)
+hipError_t launch_clip_scale(const ClipTable &t, const ClipSums &c, bool first_table, hipStream_t s)
 {
-    hipLaunchKernelGGL(clip_scale_kernel, dim3(t.blocks), dim3(kThreads), 0, s, t, factor);
+    if (c.blocks <= kClipFew)
+        hipLaunchKernelGGL(clip_scale_kernel<true>, dim3(t.blocks), dim3(kThreads), 0, s, t, c, first_table);
+    else
+        hipLaunchKernelGGL(clip_scale_kernel<false>, dim3(t.blocks), dim3(kThreads), 0, s, t, c, 0);
     return hipGetLastError();
 }
 

@@ -112,6 +112,7 @@ struct NormGradArgs {
     const uint16_t *dr, *dz;
     uint16_t *dx, *dy;
     float *d_token;            // gate gradient of tokens [T], or null
+    float4 *stats;             // [T] for rows of more than 8192 columns
     float *partial;            // [blocks, sums, H]
     int post_at, pre_at, gate_at;  // place of each column sum, -1: not wanted
     int sums;
@@ -119,12 +120,12 @@ struct NormGradArgs {
     float eps, alpha, offset;
 };
 int norm_grad_blocks(int T, int H);
+size_t norm_grad_stats_bytes(int T, int H);
 hipError_t launch_block_norm_backward(const NormGradArgs &a, hipStream_t s);
 
 // ---- clipping -------------------------------------------------------------
 
 constexpr int kClipTensors = 112;   // tensors of one launch: the table is a kernel argument
-constexpr int kClipChunk = 32768;   // elements of one block
 
 struct ClipTensor {
     const void *data;
@@ -138,13 +139,25 @@ struct ClipTable {
     ClipTensor t[kClipTensors];
     int count;
     int blocks;
+    int chunk;                 // elements of one block
 };
 
-// partial[block] = sum of squares of the block's chunk
+// What all blocks of a call share: partial[block] = sum of squares of the block's chunk,
+// and what comes of their sum.
+struct ClipSums {
+    double *partial;
+    int64_t blocks;            // of all launches
+    float *norm;
+    float *factor;             // 1: leave the values as they are
+    float max_norm;
+};
+
 hipError_t launch_clip_squares(const ClipTable &t, double *partial, hipStream_t s);
-// norm and the factor (1: leave as they are) from all partial sums
-hipError_t launch_clip_norm(const double *partial, int64_t blocks, float max_norm, float *norm,
-                            float *factor, hipStream_t s);
-hipError_t launch_clip_scale(const ClipTable &t, const float *factor, hipStream_t s);
+// Norm and factor from all partial sums, needed before the scaling of more than
+// kClipFew blocks; fewer are summed by each scaling block, the first of which
+// (`first_table`) writes the norm.
+constexpr int64_t kClipFew = 4096;
+hipError_t launch_clip_norm(const ClipSums &c, hipStream_t s);
+hipError_t launch_clip_scale(const ClipTable &t, const ClipSums &c, bool first_table, hipStream_t s);
 
 } // namespace moe_lora

@@ -191,11 +191,13 @@ def test_norm_backward_arguments(lib):
 
 
 def test_norm_workspace_is_bounded(lib):
-    """Column sums of at most one block per CU."""
-    for H in (64, 2048, 65536):
-        sizes = [binding.block_norm_backward_workspace_size(_norm_shape(rows=T, hidden=H))
-                 for T in (0, 1, 100, 10000, 1 << 24)]
-        assert sizes == sorted(sizes) and sizes[-1] <= 256 * 3 * H * 4 and sizes[0] >= 3 * H * 4
+    """Column sums of as many blocks as run at once; of wide rows 16 bytes each too."""
+    for H, most in ((64, 512), (2048, 512), (4160, 256), (8192, 256), (8256, 128), (65536, 128)):
+        rows = (0, 1, 100, 10000, 1 << 24)
+        sizes = [binding.block_norm_backward_workspace_size(_norm_shape(rows=T, hidden=H)) for T in rows]
+        assert sizes == sorted(sizes) and sizes[0] >= 3 * H * 4
+        for T, size in zip(rows, sizes):
+            assert size <= most * 3 * H * 4 + (16 * T + 256 if H > 8192 else 0)
 
 
 # ---------------------------------------------------------------- clipping
@@ -242,9 +244,11 @@ def test_clip_overlaps(lib):
 
 
 def test_clip_workspace(lib):
-    for sizes in ([0], [1], [32768], [32769], [5, 70000, 1 << 35]):
+    """A sum for each block: of 2048 to 32768 elements, by how many there are in all."""
+    for sizes, chunk in (([0], 2048), ([1], 2048), ([2048], 2048), ([2049, 7], 2048), ([1 << 21, 1], 4096),
+                         ([1 << 26], 32768), ([5, 70000, 1 << 35], 32768)):
         table = (Gradient * len(sizes))(*[Gradient(4096, 4096, n, 0, 0) for n in sizes])
-        chunks = sum(-(-n // 32768) for n in sizes)
+        chunks = sum(-(-n // chunk) for n in sizes)
         need = lib.moe_lora_clip_workspace_size(table, len(sizes))
         assert need == 256 + -(-chunks * 8 // 256) * 256
 

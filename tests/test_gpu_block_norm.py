@@ -48,7 +48,8 @@ def _forward(T, H, gate="none", alpha=1.0, offset=0.0, post=True, pre=True, x=Tr
     return d, r, z
 
 
-WIDTHS = [64, 512, 576, 1024, 1088, 2048, 2112, 4096, 5120, 8192, 8256, 16384, 20480, 32768, 65536]
+WIDTHS = [64, 128, 192, 256, 320, 512, 576, 1024, 1088, 1536, 2048, 2112, 2816, 3584, 4096, 5120, 6144, 7168, 8192,
+          8256, 16384, 20480, 32768, 65536]
 
 
 @pytest.mark.parametrize("H", WIDTHS)
