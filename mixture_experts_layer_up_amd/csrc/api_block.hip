@@ -102,8 +102,13 @@ struct ForwardLayout {
     }
 };
 
+// The two gradient products go together with the smallest tiles where that costs no more
+// than a launch: neither then fills the chip for long, and each takes the other's idle
+// CUs (100 rows, 1024 terms, 512 columns 15.4 -> 12.5 us).
 struct BackwardLayout {
     ProductPlan dx, dw;
+    ProductPlan both_dx, both_dw;
+    bool together;
     int strips;
     bool makes_dz;             // dz is not d_out as it is
     size_t weight, dz, bias, partial, total;
@@ -112,7 +117,10 @@ struct BackwardLayout {
         const int64_t M = std::max<int64_t>(z.M, 1);
         dx = plan_product(M, z.K, z.columns(), false);
         dw = plan_product(z.K, z.columns(), M, false);
-        strips = act_grad_blocks(z.M, z.N);
+        const ProductPlan sx = plan_product(M, z.K, z.columns(), false, kSmallestTile);
+        const ProductPlan sw = plan_product(z.K, z.columns(), M, false, kSmallestTile);
+        together = sx.splits == 1 && sx.us + sw.us <= dx.us + dw.us + 4.0f;
+        strips = act_grad_blocks(z.M);
         makes_dz = s->activation != MOE_LORA_ACT_NONE || s->out_fp32 || z.padded();
         size_t o = 0;
         auto take = [&](size_t bytes) {
@@ -124,7 +132,10 @@ struct BackwardLayout {
         dz = take(makes_dz ? (size_t)z.M * z.columns() * 2 : 0);
         bias = take((size_t)strips * z.width() * sizeof(float));
         // the two products run one after the other
-        partial = take(std::max(split_bytes(dx, M, z.K), split_bytes(dw, z.K, z.columns())));
+        partial = take(std::max({split_bytes(dx, M, z.K), split_bytes(dw, z.K, z.columns()),
+                                 together ? split_bytes(sw, z.K, z.columns()) : 0}));
+        both_dx = sx;
+        both_dw = sw;
         total = o;
     }
 };
@@ -169,7 +180,7 @@ int chunk_of(const moe_lora_gradient *g, int32_t count)
     for (int32_t i = 0; i < count; ++i)
         n += g[i].elements;
     int chunk = 2048;
-    while (chunk < 32768 && n > chunk * (int64_t)1024)
+    while (chunk < kClipLargest && n > chunk * (int64_t)1024)
         chunk *= 2;
     return chunk;
 }
@@ -328,7 +339,8 @@ int moe_lora_linear_backward(const moe_lora_linear_shape *shape, const void *x, 
         g.d_out = d_out;
         g.preact = act ? static_cast<const uint16_t *>(preact) : nullptr;
         g.dz = makes_dz ? reinterpret_cast<uint16_t *>(ws + layout.dz) : nullptr;
-        g.partial = d_bias ? reinterpret_cast<float *>(ws + layout.bias) : nullptr;
+        // one strip's sums are the sums
+        g.partial = !d_bias ? nullptr : layout.strips == 1 ? d_bias : reinterpret_cast<float *>(ws + layout.bias);
         g.d_bias = d_bias;
         g.M = z.M;
         g.N = z.N;
@@ -343,22 +355,20 @@ int moe_lora_linear_backward(const moe_lora_linear_shape *shape, const void *x, 
     }
     const auto *wp = static_cast<const uint16_t *>(w);
     float *partial = reinterpret_cast<float *>(ws + layout.partial);
-    // d_w first: d_x may be x, which only d_w reads
+    ProductArgs gw{}, gx{};
     if (d_w) {
-        ProductArgs a{};
-        a.Q = static_cast<const uint16_t *>(x);
-        a.P = dz;
-        a.M = a.ldq = (int)z.K;
-        a.C = a.ldp = (int)z.columns();
-        a.K = (int)z.M;
-        a.partial = partial;
-        a.e.out = d_w;
-        a.e.N = z.padded() ? z.N : (int)z.columns();
-        a.e.half = z.half;
-        a.e.sets = z.sets;
-        a.e.padded = z.padded();
-        a.e.wide = wide_epilogue(a.e);
-        MOE_TRY(check(launch_product(Product::weight_grad, layout.dw, a, st)));
+        gw.Q = static_cast<const uint16_t *>(x);
+        gw.P = dz;
+        gw.M = gw.ldq = (int)z.K;
+        gw.C = gw.ldp = (int)z.columns();
+        gw.K = (int)z.M;
+        gw.partial = partial;
+        gw.e.out = d_w;
+        gw.e.N = z.padded() ? z.N : (int)z.columns();
+        gw.e.half = z.half;
+        gw.e.sets = z.sets;
+        gw.e.padded = z.padded();
+        gw.e.wide = wide_epilogue(gw.e);
     }
     if (d_x && z.M > 0) {
         if (z.padded()) {
@@ -366,19 +376,24 @@ int moe_lora_linear_backward(const moe_lora_linear_shape *shape, const void *x, 
             MOE_TRY(check(launch_pad_columns(wp, copy, z.K, z.N, z.half, z.sets, st)));
             wp = copy;
         }
-        ProductArgs a{};
-        a.Q = dz;
-        a.P = wp;
-        a.M = (int)z.M;
-        a.C = (int)z.K;
-        a.K = a.ldq = a.ldp = (int)z.columns();
-        a.partial = partial;
-        a.e.out = d_x;
-        a.e.N = a.e.half = (int)z.K;
-        a.e.sets = 1;
-        a.e.wide = wide_epilogue(a.e);
-        MOE_TRY(check(launch_product(Product::input_grad, layout.dx, a, st)));
+        gx.Q = dz;
+        gx.P = wp;
+        gx.M = (int)z.M;
+        gx.C = (int)z.K;
+        gx.K = gx.ldq = gx.ldp = (int)z.columns();
+        gx.partial = partial;
+        gx.e.out = d_x;
+        gx.e.N = gx.e.half = (int)z.K;
+        gx.e.sets = 1;
+        gx.e.wide = wide_epilogue(gx.e);
     }
+    // together unless d_x overwrites x, which d_w reads: then d_w comes first
+    if (gw.M > 0 && gx.M > 0 && d_x != x && layout.together)
+        return check(launch_both_gradients(layout.both_dw, gw, layout.both_dx, gx, st));
+    if (gw.M > 0)
+        MOE_TRY(check(launch_product(Product::weight_grad, layout.dw, gw, st)));
+    if (gx.M > 0)
+        MOE_TRY(check(launch_product(Product::input_grad, layout.dx, gx, st)));
     return MOE_LORA_OK;
 }
 

@@ -54,8 +54,13 @@ struct ProductPlan {
     int tiles_m, tiles_n, splits, k_per;
     float us;      // estimate, without a launch's own time
 };
-ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated);
+constexpr int kSmallestTile = 3;
+ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated, int only_tile = -1);
 hipError_t launch_product(Product kind, const ProductPlan &plan, const ProductArgs &a, hipStream_t s);
+// The weight's and the input's gradient in one launch (both with the smallest tiles, the
+// input's whole).
+hipError_t launch_both_gradients(const ProductPlan &dw, const ProductArgs &w, const ProductPlan &dx,
+                                 const ProductArgs &x, hipStream_t s);
 
 // The forward product for few rows or few outputs: the weight as given, any N.
 struct RowsArgs {
@@ -86,7 +91,7 @@ struct ActGradArgs {
     int N, half, sets, act, fp32;
     int blocks;                // row strips
 };
-int act_grad_blocks(int64_t M, int N);
+int act_grad_blocks(int64_t M);
 hipError_t launch_act_grad(const ActGradArgs &a, hipStream_t s);
 
 // out[q][c] = sum over r of in[r, q, c], q < sums <= 3, r in a fixed order: joins
@@ -125,7 +130,8 @@ hipError_t launch_block_norm_backward(const NormGradArgs &a, hipStream_t s);
 
 // ---- clipping -------------------------------------------------------------
 
-constexpr int kClipTensors = 112;   // tensors of one launch: the table is a kernel argument
+constexpr int kClipTensors = 112;     // tensors of one launch: the table is a kernel argument
+constexpr int kClipLargest = 32768;   // elements of a block, at most
 
 struct ClipTensor {
     const void *data;

@@ -134,10 +134,12 @@ __global__ __launch_bounds__(256) void pad_columns_kernel(const uint16_t *w, uin
 
 } // namespace
 
-int act_grad_blocks(int64_t M, int N)
+// Strips of rows: a row a thread as far as 256 strips go (1000 x 1024 values with four
+// rows a thread, one after the other: 8.8 us instead of 5.6; 512 strips of 8192 rows
+// cost more in the joining than they save).
+int act_grad_blocks(int64_t M)
 {
-    (void)N;
-    const int64_t strips = (M + 4 * kTY - 1) / (4 * kTY);
+    const int64_t strips = (M + kTY - 1) / kTY;
     return strips < 1 ? 1 : strips < 256 ? (int)strips : 256;
 }
 
@@ -148,7 +150,7 @@ hipError_t launch_act_grad(const ActGradArgs &a, hipStream_t s)
     hipLaunchKernelGGL(act_grad_kernel, dim3(a.blocks, (a.half + kTX * 4 - 1) / (kTX * 4)), dim3(kTX * kTY), 0,
                        s, a, wide);
     const hipError_t rc = hipGetLastError();
-    if (rc != hipSuccess || !a.d_bias)
+    if (rc != hipSuccess || !a.d_bias || a.partial == a.d_bias)
         return rc;
     return launch_column_sums(a.partial, a.blocks, 1, a.sets * a.N, &a.d_bias, s);
 }

@@ -110,26 +110,31 @@ enum Store {
                // and up, it is BN / 2 outputs wide
 };
 
-// WM x WN waves share the tile.
+// LDS of a block: its ring of buffers, and after the loop the waves' slabs.
+template <int BM, int BN, int STAGES, int WM, int WN>
+struct Shared {
+    static constexpr int kBuffer = (BM + BN) * BK * 2;
+    static constexpr int kRing = STAGES * kBuffer;
+    static constexpr int kSlab = BM / WM < 64 ? BM / WM : 64;   // rows a wave turns around at once
+    static constexpr int kTurn = BN / WN + 4;                   // floats of such a row: banks shift by 4 a row
+    static constexpr int kTurns = WM * WN * kSlab * kTurn * 4;
+    static constexpr int kBytes = kRing > kTurns ? kRing : kTurns;
+};
+
+// Work item `item` of a product by WM x WN waves.
 template <int BM, int BN, int STAGES, int WM, int WN, bool QS, bool PS, Store STORE>
-__global__ __launch_bounds__(WM *WN * 64, 2) void product_kernel(ProductArgs a)
+__device__ __forceinline__ void product(const ProductArgs &a, char *lds, int item)
 {
+    using S = Shared<BM, BN, STAGES, WM, WN>;
     constexpr bool GATED = STORE == kGated;
     constexpr int NT = WM * WN * 64;
-    constexpr int kQ = BM * BK * 2, kP = BN * BK * 2, kBuffer = kQ + kP;
+    constexpr int kQ = BM * BK * 2, kBuffer = S::kBuffer, kRing = S::kRing;
     constexpr int MT = BM / WM / 16, NTL = BN / WN / 16;
-    constexpr int kSlab = MT * 16 < 64 ? MT * 16 : 64;   // rows a wave turns around at once
-    constexpr int kTurn = NTL * 16 + 4;                  // floats of such a row: banks shift by 4 a row
-    constexpr int kTurns = WM * WN * kSlab * kTurn * 4;
-    constexpr int kRing = STAGES * kBuffer;
-    __shared__ __attribute__((aligned(1024))) char lds[kRing > kTurns ? kRing : kTurns];
+    constexpr int kSlab = S::kSlab, kTurn = S::kTurn;
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
 
     // consecutive tiles of one XCD are neighbours in both directions
     const int tiles = a.tiles_m * a.tiles_n;
-    const int item = xcd_balanced_item(blockIdx.x, tiles * a.splits);
-    if (item < 0)
-        return;
     const int split = item / tiles, tile = item - split * tiles;
     constexpr int kBand = 8;
     const int band = tile / (kBand * a.tiles_n);
@@ -293,6 +298,33 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void product_kernel(ProductArgs a)
     }
 }
 
+template <int BM, int BN, int STAGES, int WM, int WN, bool QS, bool PS, Store STORE>
+__global__ __launch_bounds__(WM *WN * 64, 2) void product_kernel(ProductArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) char lds[Shared<BM, BN, STAGES, WM, WN>::kBytes];
+    const int item = xcd_balanced_item(blockIdx.x, a.tiles_m * a.tiles_n * a.splits);
+    if (item >= 0)
+        product<BM, BN, STAGES, WM, WN, QS, PS, STORE>(a, lds, item);
+}
+
+// Both gradients in one launch: x_blocks blocks for the input's, which are the longer
+// ones, then those of the weight's, either spread over the XCDs by itself.
+template <int BM, int BN, int STAGES, int WM, int WN, Store STORE>
+__global__ __launch_bounds__(WM *WN * 64, 2) void both_gradients_kernel(ProductArgs w, ProductArgs x, int x_blocks)
+{
+    __shared__ __attribute__((aligned(1024))) char lds[Shared<BM, BN, STAGES, WM, WN>::kBytes];
+    const int block = blockIdx.x;
+    if (block < x_blocks) {
+        const int item = xcd_balanced_item(block, x.tiles_m * x.tiles_n);
+        if (item >= 0)
+            product<BM, BN, STAGES, WM, WN, false, false, kPlain>(x, lds, item);
+    } else {
+        const int item = xcd_balanced_item(block - x_blocks, w.tiles_m * w.tiles_n * w.splits);
+        if (item >= 0)
+            product<BM, BN, STAGES, WM, WN, true, true, STORE>(w, lds, item);
+    }
+}
+
 // Sums the splits and finishes: a thread per four columns of a row.
 __global__ __launch_bounds__(256) void join_kernel(ProductArgs a)
 {
@@ -350,6 +382,7 @@ struct Tile {
 };
 constexpr Tile kTiles[] = {{256, 256, 1.15f, 1.45f}, {256, 128, 0.65f, 0.92f}, {128, 128, 0.55f, 0.42f},
                            {64, 64, 0.20f, 0.20f}};
+static_assert(sizeof(kTiles) / sizeof(kTiles[0]) == kSmallestTile + 1, "the last tile is the smallest");
 constexpr int kCus = 256;
 
 template <int BM, int BN, int STAGES, int WM, int WN>
@@ -391,11 +424,13 @@ hipError_t launch_tile(Product kind, const ProductArgs &a, hipStream_t s)
 // sums are written and read again, at about 5 TB/s, and a second kernel starts after
 // the first (3 us): 2048 x 1536 sums of 8192 terms take 87 us whole (128 x 128 tiles),
 // 61 us as two splits of 256 x 128 tiles, 83 us as six.
-ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated)
+ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated, int only_tile)
 {
     const int64_t steps = (K + BK - 1) / BK;
     ProductPlan best{};
     for (int t = 0; t < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++t) {
+        if (only_tile >= 0 && t != only_tile)
+            continue;
         const Tile &tile = kTiles[t];
         const int64_t tiles = ((M + tile.rows - 1) / tile.rows) * ((C + tile.columns - 1) / tile.columns);
         int64_t last = 0;
@@ -427,24 +462,56 @@ ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated)
     return best;
 }
 
-hipError_t launch_product(Product kind, const ProductPlan &plan, const ProductArgs &given, hipStream_t s)
+namespace {
+
+ProductArgs with_plan(const ProductArgs &given, const ProductPlan &plan)
 {
     ProductArgs a = given;
     a.tiles_m = plan.tiles_m;
     a.tiles_n = plan.tiles_n;
     a.splits = plan.splits;
     a.k_per = plan.k_per;
-    hipError_t rc = plan.tile == 0   ? launch_tile<256, 256, 2, 2, 4>(kind, a, s)
-                    : plan.tile == 1 ? launch_tile<256, 128, 3, 4, 2>(kind, a, s)
-                    : plan.tile == 2 ? launch_tile<128, 128, 2, 2, 2>(kind, a, s)
-                                     : launch_tile<64, 64, 4, 2, 2>(kind, a, s);
-    if (rc != hipSuccess || a.splits == 1)
-        return rc;
-    const bool gated = kind == Product::forward && a.e.act == MOE_LORA_ACT_SWIGLU;
+    return a;
+}
+
+hipError_t launch_join(const ProductArgs &a, hipStream_t s)
+{
+    const bool gated = a.e.act == MOE_LORA_ACT_SWIGLU;
     const int64_t items = (int64_t)a.M * (gated ? a.e.half : a.C) / (a.e.wide ? 8 : 1);
     const int64_t blocks = (items + 255) / 256;
     hipLaunchKernelGGL(join_kernel, dim3(blocks < 1 << 20 ? blocks : 1 << 20), dim3(256), 0, s, a);
     return hipGetLastError();
+}
+
+} // namespace
+
+hipError_t launch_product(Product kind, const ProductPlan &plan, const ProductArgs &given, hipStream_t s)
+{
+    const ProductArgs a = with_plan(given, plan);
+    const hipError_t rc = plan.tile == 0   ? launch_tile<256, 256, 2, 2, 4>(kind, a, s)
+                          : plan.tile == 1 ? launch_tile<256, 128, 3, 4, 2>(kind, a, s)
+                          : plan.tile == 2 ? launch_tile<128, 128, 2, 2, 2>(kind, a, s)
+                                           : launch_tile<64, 64, 4, 2, 2>(kind, a, s);
+    return rc != hipSuccess || a.splits == 1 ? rc : launch_join(a, s);
+}
+
+hipError_t launch_both_gradients(const ProductPlan &dw, const ProductArgs &w_given, const ProductPlan &dx,
+                                 const ProductArgs &x_given, hipStream_t s)
+{
+    const ProductArgs w = with_plan(w_given, dw), x = with_plan(x_given, dx);
+    const int x_blocks = (x.tiles_m * x.tiles_n + 7) / 8 * 8;
+    const dim3 grid(x_blocks + (w.tiles_m * w.tiles_n * w.splits + 7) / 8 * 8), block(256);
+    if (w.splits > 1)
+        hipLaunchKernelGGL((both_gradients_kernel<64, 64, 4, 2, 2, kPartial>), grid, block, 0, s, w, x,
+                           x_blocks);
+    else if (w.e.wide && !w.e.padded)
+        hipLaunchKernelGGL((both_gradients_kernel<64, 64, 4, 2, 2, kPlain>), grid, block, 0, s, w, x,
+                           x_blocks);
+    else
+        hipLaunchKernelGGL((both_gradients_kernel<64, 64, 4, 2, 2, kFull>), grid, block, 0, s, w, x,
+                           x_blocks);
+    const hipError_t rc = hipGetLastError();
+    return rc != hipSuccess || w.splits == 1 ? rc : launch_join(w, s);
 }
 
 } // namespace moe_lora

@@ -132,3 +132,10 @@ def test_refusals():
         binding.clip_gradients([g[0], torch.zeros(100, device="cuda")], 1.0, out=[torch.zeros(100, device="cuda"), g[0]])
     with pytest.raises(binding.MoELoRAError, match="workspace"):
         binding.clip_gradients(g, 1.0, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
+def test_many_values():
+    """More than 16 M values, whose results are written past the caches."""
+    announce("clip 20 M values")
+    _check(_grads([17_000_001, 3_000_003, 5], seed=8), 1.0)
+    _check(_grads([17_000_001, 3_000_003, 5], seed=8), 1.0, in_place=True)

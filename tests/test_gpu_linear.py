@@ -198,7 +198,7 @@ def test_parts_alone_are_the_same_bits():
         assert torch.equal(one[name], every[name])
         assert all(v is None for k, v in one.items() if k != name)
     again = binding.linear_backward(shape, x, w, d, preact=pre, bias_grad=True, d_x=x)   # in place
-    assert all(torch.equal(again[k], every[k]) for k in every)
+    assert again["d_x"] is x and all(torch.equal(again[k], every[k]) for k in every)
 
 
 def test_no_rows():
