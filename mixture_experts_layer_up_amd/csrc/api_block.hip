@@ -185,6 +185,17 @@ int chunk_of(const moe_lora_gradient *g, int32_t count)
     return chunk;
 }
 
+// More than the second-level caches hold (32 MB) is written past them: they and the last
+// level then still have what the squares have read (60 tensors, 111 MB, in turn with
+// others: 79.5 -> 68.5 us).  Less stays in them for its reader.
+bool past_caches(const moe_lora_gradient *g, int32_t count)
+{
+    int64_t bytes = 0;
+    for (int32_t i = 0; i < count; ++i)
+        bytes += g[i].elements * (g[i].fp32 ? 4 : 2);
+    return bytes > 32 << 20;
+}
+
 int64_t total_chunks(const moe_lora_gradient *g, int32_t count, int chunk)
 {
     int64_t n = 0;
@@ -232,6 +243,7 @@ int for_tables(const moe_lora_gradient *g, int32_t count, int chunk, F f)
 {
     ClipTable t;
     t.chunk = chunk;
+    t.stream = past_caches(g, count);
     t.count = t.blocks = 0;
     int64_t done = 0;
     for (int32_t i = 0; i <= count; ++i) {

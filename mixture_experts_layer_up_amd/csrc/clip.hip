@@ -220,9 +220,6 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable t, ClipS
     } else {
         f = *c.factor;
     }
-    // more than 16 M values: written past the caches, which then still hold what the squares
-    // have read (60 tensors, 222 MB in turn with others: 79.5 -> 68.5 us)
-    const bool stream = t.chunk == kClipLargest;
     const int i = find_tensor(t, blockIdx.x);
     if (f == 1.0f && t.t[i].out == t.t[i].data)
         return;
@@ -230,9 +227,9 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable t, ClipS
     const int64_t left = t.t[i].n - at;
     const int n = left < t.chunk ? (int)left : t.chunk;
     if (t.t[i].fp32)
-        chunk_scale<1>(t.t[i].data, t.t[i].out, at, n, f, stream);
+        chunk_scale<1>(t.t[i].data, t.t[i].out, at, n, f, t.stream);
     else
-        chunk_scale<0>(t.t[i].data, t.t[i].out, at, n, f, stream);
+        chunk_scale<0>(t.t[i].data, t.t[i].out, at, n, f, t.stream);
 }
 
 } // namespace

@@ -146,6 +146,7 @@ struct ClipTable {
     int count;
     int blocks;
     int chunk;                 // elements of one block
+    bool stream;               // results are written past the caches
 };
 
 // What all blocks of a call share: partial[block] = sum of squares of the block's chunk,

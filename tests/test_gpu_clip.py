@@ -135,7 +135,8 @@ def test_refusals():
 
 
 def test_many_values():
-    """More than 16 M values, whose results are written past the caches."""
-    announce("clip 20 M values")
-    _check(_grads([17_000_001, 3_000_003, 5], seed=8), 1.0)
-    _check(_grads([17_000_001, 3_000_003, 5], seed=8), 1.0, in_place=True)
+    """More than 32 MB, whose results are written past the caches; the largest blocks."""
+    for sizes in ([9_000_001, 3_000_003, 5], [17_000_001, 3_000_003, 5]):
+        announce(f"clip {sizes}")
+        _check(_grads(sizes, seed=8), 1.0)
+        _check(_grads(sizes, seed=8), 1.0, in_place=True)
