@@ -110,8 +110,10 @@ __device__ __forceinline__ double chunk_squares(const void *data, int64_t at, in
     return s;
 }
 
-template <int F32>
-__device__ __forceinline__ void chunk_scale(const void *data, void *out, int64_t at, int n, float c, bool stream)
+// STREAM is a template argument: of two stores under a branch the compiler makes one,
+// without the hint.
+template <int F32, bool STREAM>
+__device__ __forceinline__ void chunk_scale(const void *data, void *out, int64_t at, int n, float c)
 {
     using E = Element<F32>;
     constexpr int kPer = F32 ? 4 : 8;
@@ -134,7 +136,7 @@ __device__ __forceinline__ void chunk_scale(const void *data, void *out, int64_t
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
             f[i] *= c;
-        if (stream)
+        if constexpr (STREAM)
             store16_stream(o + head + w * kPer, pack<F32>(f));
         else
             store16(o + head + w * kPer, pack<F32>(f));
@@ -208,7 +210,7 @@ __global__ __launch_bounds__(kNormThreads) void clip_norm_kernel(ClipSums c)
 // FEW: the blocks sum the partial sums themselves (up to 4096, 32 KB from the cache) and
 // save a launch: 5 tensors of 0.3 M elements 7.6 us in kernels, 14.3 with it (and chunks
 // of 32768).
-template <bool FEW>
+template <bool FEW, bool STREAM>
 __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable t, ClipSums c, int first_table)
 {
     float f;
@@ -227,9 +229,9 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable t, ClipS
     const int64_t left = t.t[i].n - at;
     const int n = left < t.chunk ? (int)left : t.chunk;
     if (t.t[i].fp32)
-        chunk_scale<1>(t.t[i].data, t.t[i].out, at, n, f, t.stream);
+        chunk_scale<1, STREAM>(t.t[i].data, t.t[i].out, at, n, f);
     else
-        chunk_scale<0>(t.t[i].data, t.t[i].out, at, n, f, t.stream);
+        chunk_scale<0, STREAM>(t.t[i].data, t.t[i].out, at, n, f);
 }
 
 } // namespace
@@ -248,10 +250,15 @@ hipError_t launch_clip_norm(const ClipSums &c, hipStream_t s)
 
 hipError_t launch_clip_scale(const ClipTable &t, const ClipSums &c, bool first_table, hipStream_t s)
 {
-    if (c.blocks <= kClipFew)
-        hipLaunchKernelGGL(clip_scale_kernel<true>, dim3(t.blocks), dim3(kThreads), 0, s, t, c, first_table);
-    else
-        hipLaunchKernelGGL(clip_scale_kernel<false>, dim3(t.blocks), dim3(kThreads), 0, s, t, c, 0);
+    const dim3 grid(t.blocks), block(kThreads);
+    if (c.blocks <= kClipFew) {
+        if (t.stream)
+            hipLaunchKernelGGL((clip_scale_kernel<true, true>), grid, block, 0, s, t, c, first_table);
+        else
+            hipLaunchKernelGGL((clip_scale_kernel<true, false>), grid, block, 0, s, t, c, first_table);
+    } else {
+        hipLaunchKernelGGL((clip_scale_kernel<false, true>), grid, block, 0, s, t, c, 0);
+    }
     return hipGetLastError();
 }
 
