@@ -102,9 +102,10 @@ struct ForwardLayout {
     }
 };
 
-// The two gradient products go together with the smallest tiles where that costs no more
-// than a launch: neither then fills the chip for long, and each takes the other's idle
-// CUs (100 rows, 1024 terms, 512 columns 15.4 -> 12.5 us).
+// The two gradient products go together where that is estimated to take no longer than
+// one after the other and a launch's 3 us: each takes the CUs that the other leaves idle
+// (100 rows, 1024 terms, 512 columns 15.4 -> 9.5 us; 4096, 2048 and 1536
+// 65 -> 53; 8192, 2048 and 1536 104 -> 98).
 struct BackwardLayout {
     ProductPlan dx, dw;
     ProductPlan both_dx, both_dw;
@@ -117,9 +118,7 @@ struct BackwardLayout {
         const int64_t M = std::max<int64_t>(z.M, 1);
         dx = plan_product(M, z.K, z.columns(), false);
         dw = plan_product(z.K, z.columns(), M, false);
-        const ProductPlan sx = plan_product(M, z.K, z.columns(), false, kSmallestTile);
-        const ProductPlan sw = plan_product(z.K, z.columns(), M, false, kSmallestTile);
-        together = sx.splits == 1 && sx.us + sw.us <= dx.us + dw.us + 4.0f;
+        together = plan_both(M, z.K, z.columns(), &both_dw, &both_dx) <= dx.us + dw.us + 3.0f;
         strips = act_grad_blocks(z.M);
         makes_dz = s->activation != MOE_LORA_ACT_NONE || s->out_fp32 || z.padded();
         size_t o = 0;
@@ -133,9 +132,7 @@ struct BackwardLayout {
         bias = take((size_t)strips * z.width() * sizeof(float));
         // the two products run one after the other
         partial = take(std::max({split_bytes(dx, M, z.K), split_bytes(dw, z.K, z.columns()),
-                                 together ? split_bytes(sw, z.K, z.columns()) : 0}));
-        both_dx = sx;
-        both_dw = sw;
+                                 together ? split_bytes(both_dw, z.K, z.columns()) : 0}));
         total = o;
     }
 };

@@ -54,11 +54,11 @@ struct ProductPlan {
     int tiles_m, tiles_n, splits, k_per;
     float us;      // estimate, without a launch's own time
 };
-constexpr int kSmallestTile = 3;
-ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated, int only_tile = -1);
+ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated);
 hipError_t launch_product(Product kind, const ProductPlan &plan, const ProductArgs &a, hipStream_t s);
-// The weight's and the input's gradient in one launch (both with the smallest tiles, the
-// input's whole).
+// The weight's and the input's gradient in one launch, with the same tiles, the input's
+// whole: M rows, `in` and `columns` of the weight.  Returns the estimated microseconds.
+float plan_both(int64_t M, int64_t in, int64_t columns, ProductPlan *dw, ProductPlan *dx);
 hipError_t launch_both_gradients(const ProductPlan &dw, const ProductArgs &w, const ProductPlan &dx,
                                  const ProductArgs &x, hipStream_t s);
 

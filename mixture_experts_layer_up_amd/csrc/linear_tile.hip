@@ -307,19 +307,22 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void product_kernel(ProductArgs a)
         product<BM, BN, STAGES, WM, WN, QS, PS, STORE>(a, lds, item);
 }
 
-// Both gradients in one launch: x_blocks blocks for the input's, which are the longer
-// ones, then those of the weight's, either spread over the XCDs by itself.
+// Both gradients in one launch: the blocks of the one with the longer ones first
+// (`first_blocks` of the grid), either spread over the XCDs by itself.
 template <int BM, int BN, int STAGES, int WM, int WN, Store STORE>
-__global__ __launch_bounds__(WM *WN * 64, 2) void both_gradients_kernel(ProductArgs w, ProductArgs x, int x_blocks)
+__global__ __launch_bounds__(WM *WN * 64, 2)
+void both_gradients_kernel(ProductArgs w, ProductArgs x, int x_first, int first_blocks)
 {
     __shared__ __attribute__((aligned(1024))) char lds[Shared<BM, BN, STAGES, WM, WN>::kBytes];
     const int block = blockIdx.x;
-    if (block < x_blocks) {
-        const int item = xcd_balanced_item(block, x.tiles_m * x.tiles_n);
+    const bool first = block < first_blocks;
+    const int mine = first ? block : block - first_blocks;
+    if (first == (x_first != 0)) {
+        const int item = xcd_balanced_item(mine, x.tiles_m * x.tiles_n);
         if (item >= 0)
             product<BM, BN, STAGES, WM, WN, false, false, kPlain>(x, lds, item);
     } else {
-        const int item = xcd_balanced_item(block - x_blocks, w.tiles_m * w.tiles_n * w.splits);
+        const int item = xcd_balanced_item(mine, w.tiles_m * w.tiles_n * w.splits);
         if (item >= 0)
             product<BM, BN, STAGES, WM, WN, true, true, STORE>(w, lds, item);
     }
@@ -376,13 +379,16 @@ __global__ __launch_bounds__(256) void join_kernel(ProductArgs a)
 // CU (most CUs busy) and among others there, measured with 2048 to 8192 rows, 1536 to
 // 4096 columns and as many terms.  Larger tiles read LDS and the second-level cache
 // less per product; smaller ones fill the chip with fewer rows.
+// `rest`: what a block takes beside its steps, on a CU with others.
 struct Tile {
     int rows, columns;
-    float alone, shared;
+    float alone, shared, rest;
 };
-constexpr Tile kTiles[] = {{256, 256, 1.15f, 1.45f}, {256, 128, 0.65f, 0.92f}, {128, 128, 0.55f, 0.42f},
-                           {64, 64, 0.20f, 0.20f}};
-static_assert(sizeof(kTiles) / sizeof(kTiles[0]) == kSmallestTile + 1, "the last tile is the smallest");
+constexpr int kTileShapes = 4;
+constexpr Tile kTiles[kTileShapes] = {{256, 256, 1.15f, 1.45f, 4.0f},
+                                      {256, 128, 0.65f, 0.92f, 3.0f},
+                                      {128, 128, 0.55f, 0.48f, 1.5f},
+                                      {64, 64, 0.20f, 0.20f, 0.5f}};
 constexpr int kCus = 256;
 
 template <int BM, int BN, int STAGES, int WM, int WN>
@@ -420,46 +426,92 @@ hipError_t launch_tile(Product kind, const ProductArgs &a, hipStream_t s)
 
 } // namespace
 
-// The tile and split that take the least time by the figures above.  A split's fp32
-// sums are written and read again, at about 5 TB/s, and a second kernel starts after
-// the first (3 us): 2048 x 1536 sums of 8192 terms take 87 us whole (128 x 128 tiles),
-// 61 us as two splits of 256 x 128 tiles, 83 us as six.
-ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated, int only_tile)
+namespace {
+
+ProductPlan cut(int t, int64_t M, int64_t C, int64_t K, int64_t splits, bool gated)
+{
+    const Tile &tile = kTiles[t];
+    const int64_t steps = (K + BK - 1) / BK, per = steps > 0 ? (steps + splits - 1) / splits : 1;
+    ProductPlan p{};
+    p.tile = t;
+    p.k_per = (int)(per * BK);
+    p.splits = steps > 0 ? (int)((steps + per - 1) / per) : 1;
+    const bool pairs = gated && p.splits == 1;
+    const int64_t width = pairs ? C / 2 : C, columns = pairs ? tile.columns / 2 : tile.columns;
+    p.tiles_m = (int)((M + tile.rows - 1) / tile.rows);
+    p.tiles_n = (int)((width + columns - 1) / columns);
+    return p;
+}
+
+int64_t blocks_of(const ProductPlan &p) { return (int64_t)p.tiles_m * p.tiles_n * p.splits; }
+
+// A split's fp32 sums are written and read again, at about 5 TB/s, and a second kernel
+// starts after the first (3 us): 2048 x 1536 sums of 8192 terms take 87 us whole (128 x
+// 128 tiles), 61 us as two splits of 256 x 128 tiles, 83 us as six.
+float joining(const ProductPlan &p, int64_t M, int64_t C)
+{
+    return p.splits > 1 ? 3.0f + (float)p.splits * M * C * 8.0f / 5e6f : 0.0f;
+}
+
+// f(splits) for every cutting of the terms that is worth a look, the whole first
+template <class F>
+void for_splits(int64_t tiles, int64_t K, F f)
 {
     const int64_t steps = (K + BK - 1) / BK;
-    ProductPlan best{};
-    for (int t = 0; t < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++t) {
-        if (only_tile >= 0 && t != only_tile)
-            continue;
-        const Tile &tile = kTiles[t];
-        const int64_t tiles = ((M + tile.rows - 1) / tile.rows) * ((C + tile.columns - 1) / tile.columns);
-        int64_t last = 0;
-        for (int64_t splits = 1; splits <= 64; ++splits) {
-            const int64_t per = (steps + splits - 1) / splits;
-            if (splits > 1 && (per < 4 || tiles * splits > 4 * kCus))
-                break;
-            if (per == last)   // the same cutting with empty splits
-                continue;
-            last = per;
-            const int64_t each = (tiles * splits + kCus - 1) / kCus;   // blocks of the busiest CU
-            float us = per * (each == 1 ? tile.alone : each * tile.shared);
-            if (splits > 1)
-                us += 3.0f + (float)splits * M * C * 8.0f / 5e6f;
-            if (best.tiles_m == 0 || us < best.us) {
-                best.us = us;
-                best.tile = t;
-                best.splits = (int)((steps + per - 1) / per);
-                best.k_per = (int)(per * BK);
-                const bool pairs = gated && best.splits == 1;
-                const int64_t width = pairs ? C / 2 : C, columns = pairs ? tile.columns / 2 : tile.columns;
-                best.tiles_m = (int)((M + tile.rows - 1) / tile.rows);
-                best.tiles_n = (int)((width + columns - 1) / columns);
-            }
-        }
+    int64_t last = 0;
+    for (int64_t splits = 1; splits <= 64; ++splits) {
+        const int64_t per = (steps + splits - 1) / splits;
+        if (splits > 1 && (per < 4 || tiles * splits > 4 * kCus))
+            return;
+        if (per != last)   // else the same cutting with empty splits
+            f(splits);
+        last = per;
     }
-    if (best.splits < 1)   // no terms
-        best.splits = 1;
+}
+
+} // namespace
+
+// The tile and split that take the least time by the figures above.
+ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated)
+{
+    ProductPlan best{};
+    for (int t = 0; t < kTileShapes; ++t) {
+        const ProductPlan whole = cut(t, M, C, K, 1, false);
+        for_splits(blocks_of(whole), K, [&](int64_t splits) {
+            ProductPlan p = cut(t, M, C, K, splits, gated);
+            const int64_t each = (blocks_of(cut(t, M, C, K, splits, false)) + kCus - 1) / kCus;   // of the busiest CU
+            const float steps = (float)(p.k_per / BK);
+            p.us = steps * (each == 1 ? kTiles[t].alone : each * kTiles[t].shared) + joining(p, M, C);
+            if (best.tiles_m == 0 || p.us < best.us)
+                best = p;
+        });
+    }
     return best;
+}
+
+// The same for the two gradients in one launch: the CUs' work in all, the longest block,
+// and what a block takes beside its steps.
+float plan_both(int64_t M, int64_t in, int64_t columns, ProductPlan *dw, ProductPlan *dx)
+{
+    float least = 0.0f;
+    for (int t = 0; t < kTileShapes; ++t) {
+        const Tile &tile = kTiles[t];
+        const ProductPlan x = cut(t, M, in, columns, 1, false), whole = cut(t, in, columns, M, 1, false);
+        for_splits(blocks_of(whole), M, [&](int64_t splits) {
+            const ProductPlan w = cut(t, in, columns, M, splits, false);
+            const float x_steps = (float)(x.k_per / BK), w_steps = (float)(w.k_per / BK);
+            const float all = (blocks_of(x) * (x_steps * tile.shared + tile.rest) +
+                               blocks_of(w) * (w_steps * tile.shared + tile.rest)) / kCus;
+            const float longest = (x_steps > w_steps ? x_steps : w_steps) * tile.alone + tile.rest;
+            const float us = (all > longest ? all : longest) + joining(w, in, columns);
+            if (least == 0.0f || us < least) {
+                least = us;
+                *dw = w;
+                *dx = x;
+            }
+        });
+    }
+    return least;
 }
 
 namespace {
@@ -495,22 +547,37 @@ hipError_t launch_product(Product kind, const ProductPlan &plan, const ProductAr
     return rc != hipSuccess || a.splits == 1 ? rc : launch_join(a, s);
 }
 
+namespace {
+
+template <int BM, int BN, int STAGES, int WM, int WN>
+hipError_t launch_both(const ProductArgs &w, const ProductArgs &x, hipStream_t s)
+{
+    auto padded = [](int64_t n) { return (int)((n + 7) / 8 * 8); };
+    const int w_blocks = padded((int64_t)w.tiles_m * w.tiles_n * w.splits), x_blocks = padded((int64_t)x.tiles_m * x.tiles_n);
+    const int x_first = x.K > w.k_per, first = x_first ? x_blocks : w_blocks;
+    const dim3 grid(w_blocks + x_blocks), block(WM * WN * 64);
+    if (w.splits > 1)
+        hipLaunchKernelGGL((both_gradients_kernel<BM, BN, STAGES, WM, WN, kPartial>), grid, block, 0, s, w, x, x_first,
+                           first);
+    else if (w.e.wide && !w.e.padded)
+        hipLaunchKernelGGL((both_gradients_kernel<BM, BN, STAGES, WM, WN, kPlain>), grid, block, 0, s, w, x, x_first,
+                           first);
+    else
+        hipLaunchKernelGGL((both_gradients_kernel<BM, BN, STAGES, WM, WN, kFull>), grid, block, 0, s, w, x, x_first,
+                           first);
+    return hipGetLastError();
+}
+
+} // namespace
+
 hipError_t launch_both_gradients(const ProductPlan &dw, const ProductArgs &w_given, const ProductPlan &dx,
                                  const ProductArgs &x_given, hipStream_t s)
 {
     const ProductArgs w = with_plan(w_given, dw), x = with_plan(x_given, dx);
-    const int x_blocks = (x.tiles_m * x.tiles_n + 7) / 8 * 8;
-    const dim3 grid(x_blocks + (w.tiles_m * w.tiles_n * w.splits + 7) / 8 * 8), block(256);
-    if (w.splits > 1)
-        hipLaunchKernelGGL((both_gradients_kernel<64, 64, 4, 2, 2, kPartial>), grid, block, 0, s, w, x,
-                           x_blocks);
-    else if (w.e.wide && !w.e.padded)
-        hipLaunchKernelGGL((both_gradients_kernel<64, 64, 4, 2, 2, kPlain>), grid, block, 0, s, w, x,
-                           x_blocks);
-    else
-        hipLaunchKernelGGL((both_gradients_kernel<64, 64, 4, 2, 2, kFull>), grid, block, 0, s, w, x,
-                           x_blocks);
-    const hipError_t rc = hipGetLastError();
+    const hipError_t rc = dw.tile == 0   ? launch_both<256, 256, 2, 2, 4>(w, x, s)
+                          : dw.tile == 1 ? launch_both<256, 128, 3, 4, 2>(w, x, s)
+                          : dw.tile == 2 ? launch_both<128, 128, 2, 2, 2>(w, x, s)
+                                         : launch_both<64, 64, 4, 2, 2>(w, x, s);
     return rc != hipSuccess || w.splits == 1 ? rc : launch_join(w, s);
 }
 
