@@ -376,7 +376,7 @@ __global__ __launch_bounds__(256) void join_kernel(ProductArgs a)
 }
 
 // Tile shapes, and the microseconds that a step of 64 terms takes a block alone on its
-// CU (most CUs busy) and among others there, measured with 2048 to 8192 rows, 1536 to
+// CU (few CUs busy) and among others, measured with 2048 to 8192 rows, 1536 to
 // 4096 columns and as many terms.  Larger tiles read LDS and the second-level cache
 // less per product; smaller ones fill the chip with fewer rows.
 // `rest`: what a block takes beside its steps, on a CU with others.
@@ -385,8 +385,8 @@ struct Tile {
     float alone, shared, rest;
 };
 constexpr int kTileShapes = 4;
-constexpr Tile kTiles[kTileShapes] = {{256, 256, 1.15f, 1.45f, 4.0f},
-                                      {256, 128, 0.65f, 0.92f, 3.0f},
+constexpr Tile kTiles[kTileShapes] = {{256, 256, 1.05f, 1.45f, 4.0f},
+                                      {256, 128, 0.60f, 0.92f, 3.0f},
                                       {128, 128, 0.55f, 0.48f, 1.5f},
                                       {64, 64, 0.20f, 0.20f, 0.5f}};
 constexpr int kCus = 256;
@@ -445,6 +445,13 @@ ProductPlan cut(int t, int64_t M, int64_t C, int64_t K, int64_t splits, bool gat
 
 int64_t blocks_of(const ProductPlan &p) { return (int64_t)p.tiles_m * p.tiles_n * p.splits; }
 
+// A step of a block alone on its CU, which takes longer as more CUs are busy.
+float alone(const Tile &tile, int64_t blocks)
+{
+    const float share = blocks < kCus ? (float)blocks / kCus : 1.0f;
+    return tile.alone + (tile.shared > tile.alone ? (tile.shared - tile.alone) * share : 0.0f);
+}
+
 // A split's fp32 sums are written and read again, at about 5 TB/s, and a second kernel
 // starts after the first (3 us): 2048 x 1536 sums of 8192 terms take 87 us whole (128 x
 // 128 tiles), 61 us as two splits of 256 x 128 tiles, 83 us as six.
@@ -481,7 +488,7 @@ ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated)
             ProductPlan p = cut(t, M, C, K, splits, gated);
             const int64_t each = (blocks_of(cut(t, M, C, K, splits, false)) + kCus - 1) / kCus;   // of the busiest CU
             const float steps = (float)(p.k_per / BK);
-            p.us = steps * (each == 1 ? kTiles[t].alone : each * kTiles[t].shared) + joining(p, M, C);
+            p.us = steps * (each == 1 ? alone(kTiles[t], blocks_of(p)) : each * kTiles[t].shared) + joining(p, M, C);
             if (best.tiles_m == 0 || p.us < best.us)
                 best = p;
         });
@@ -502,7 +509,8 @@ float plan_both(int64_t M, int64_t in, int64_t columns, ProductPlan *dw, Product
             const float x_steps = (float)(x.k_per / BK), w_steps = (float)(w.k_per / BK);
             const float all = (blocks_of(x) * (x_steps * tile.shared + tile.rest) +
                                blocks_of(w) * (w_steps * tile.shared + tile.rest)) / kCus;
-            const float longest = (x_steps > w_steps ? x_steps : w_steps) * tile.alone + tile.rest;
+            const float longest = (x_steps > w_steps ? x_steps : w_steps) * alone(tile, blocks_of(x) + blocks_of(w)) +
+                                  tile.rest;
             const float us = (all > longest ? all : longest) + joining(w, in, columns);
             if (least == 0.0f || us < least) {
                 least = us;
