@@ -328,7 +328,8 @@ void both_gradients_kernel(ProductArgs w, ProductArgs x, int x_first, int first_
     }
 }
 
-// Sums the splits and finishes: a thread per four columns of a row.
+// Sums the splits, ascending, and finishes: a thread per eight columns of a row (one
+// where N or the pointers do not allow eight).
 __global__ __launch_bounds__(256) void join_kernel(ProductArgs a)
 {
     const bool gated = a.e.act == MOE_LORA_ACT_SWIGLU;

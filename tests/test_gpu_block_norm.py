@@ -152,9 +152,9 @@ def test_backward_parts(gate, post, d_r, d_z, y):
 @pytest.mark.parametrize("gate", ["token", "channel"])
 def test_backward_parts_alone_and_in_place(gate):
     announce("block_norm_backward parts alone")
-    for H in (128, 2048):
-        d, every = _backward(300, H, gate)
-        sh = _shape(300, H, gate)
+    for T, H in ((300, 128), (300, 2048), (40, 1088), (30, 8256), (30, 16384)):
+        d, every = _backward(T, H, gate)
+        sh = _shape(T, H, gate)
         kw = dict(post_weight=d["w_post"], pre_weight=d["w_pre"], gate=d["gate"])
         for name in every:
             one = binding.block_norm_backward(sh, d["x"], d["y"], d_residual=d["d_r"], d_normed=d["d_z"],
