@@ -184,6 +184,14 @@ def clip(gradients, max_norm):
     return total, f, [g.double() * f for g in gradients]
 
 
+def apart(got, want):
+    """2-norm of the difference over that of the values: a worst case over thousands of
+    terms hides a lost step of them, this does not.  A rounding to bf16 stays below U16,
+    one of an operand as well (its errors have random signs)."""
+    n = float(want.norm())
+    return float((got.double() - want).norm()) / n if n else 0.0
+
+
 def worst(got, want, bound):
     """Largest share of the bound that is used (NaN fails)."""
     d = (got.double() - want).abs() / bound

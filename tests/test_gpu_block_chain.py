@@ -221,7 +221,7 @@ class _Linear(torch.autograd.Function):
 
 
 def test_autograd_function_around_a_product():
-    """As a torch user wraps it: broadcast gradients arrive, leaves accumulate, captured while eager graphs live."""
+    """As a torch user wraps it: a broadcast gradient arrives and is made contiguous."""
     announce("linear in autograd")
     g = torch.Generator("cuda").manual_seed(6)
     sh = binding.LinearShape(50, 64, 24, 4, 0)

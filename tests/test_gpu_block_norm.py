@@ -41,10 +41,10 @@ def _forward(T, H, gate="none", alpha=1.0, offset=0.0, post=True, pre=True, x=Tr
     r, z = binding.block_norm(_shape(T, H, gate, alpha, offset), x, y, post_weight=w_post, pre_weight=w_pre,
                               gate=d["gate"])
     want_r, off_r, want_z, off_z = _block.norm(x, y, w_post, w_pre, d["wide"], EPS, alpha, offset)
-    assert _block.worst(r, want_r, off_r) <= 1
+    assert _block.worst(r, want_r, off_r) <= 1 and _block.apart(r, want_r) <= _block.U16
     assert (z is None) == (not pre)
     if pre:
-        assert _block.worst(z, want_z, off_z) <= 1
+        assert _block.worst(z, want_z, off_z) <= 1 and _block.apart(z, want_z) <= _block.U16
     return d, r, z
 
 
@@ -126,6 +126,8 @@ def _backward(T, H, gate="none", alpha=1.0, offset=0.0, post=True, d_r=True, d_z
             v, off = want[name]
             share = _block.worst(got[name].view(v.shape), v, off)
             assert share <= 1, (name, share)
+            near = _block.U16 if got[name].dtype == torch.bfloat16 else 1e-5
+            assert _block.apart(got[name].view(v.shape), v) <= near, name
     return d, got
 
 

@@ -47,6 +47,8 @@ def _forward(M, K, N, act, fp32=False, bias=True, residual=True, preact=True, se
     assert got is out and out_ok() and z_ok()
     want, bound, pre, pre_bound = _block.linear(x, w, act, b, res, fp32)
     assert _block.worst(out, want, bound) <= 1
+    if M * N >= 64:
+        assert _block.apart(out, want) <= (1e-5 if fp32 else _block.U16)
     if preact:
         assert _block.worst(z, pre, pre_bound) <= 1
 
@@ -74,6 +76,16 @@ def test_forward_large(M, K, N, act):
     """Every tile shape, sums split and whole, rows of a few users over wide weights."""
     _forward(M, K, N, act, bias=False, residual=False, preact=False)
     _forward(M, K, N, act, seed=2)
+
+
+# sizes that reach every tile with every way to store it (whole with an epilogue, whole
+# swiglu pairs, split sums of one and of two projections), and every body for few rows
+@pytest.mark.parametrize("M,K,N,act", [
+    (20, 8, 2056, "swiglu"), (8193, 8, 500, "swiglu"), (6000, 8192, 500, "none"), (6000, 8192, 250, "swiglu"),
+    (8193, 8, 250, "swiglu"), (4097, 4096, 264, "gelu"), (6000, 4096, 99, "swiglu"), (8193, 8, 250, "silu"),
+    (3000, 8192, 99, "none"), (4097, 4096, 99, "swiglu"), (8193, 8, 8, "swiglu"), (20, 8192, 1, "swiglu")])
+def test_forward_every_body(M, K, N, act):
+    _forward(M, K, N, act)
 
 
 @pytest.mark.parametrize("M,N", [(5, 96), (300, 96), (2048, 100), (2048, 2048)])
@@ -150,6 +162,8 @@ def _backward(M, K, N, act, fp32=False, bias=True, seed=11):
             continue
         share = _block.worst(t, *want[name])
         assert share <= 1, (name, share)
+        if t.numel() >= 64:
+            assert _block.apart(t, want[name][0]) <= (1e-5 if name == "d_bias" else 2 * _block.U16), name
 
 
 @pytest.mark.parametrize("act", _block.ACTS)
@@ -166,6 +180,18 @@ def test_backward(M, K, N, act):
                                                  (2048, 4104, 64, "none", False, False)])
 def test_backward_large(M, K, N, act, fp32, bias):
     _backward(M, K, N, act, fp32, bias)
+
+
+# the same for the gradients: one launch for both or one each, whole or split, plain or padded
+@pytest.mark.parametrize("M,K,N,act", [
+    (1000, 8192, 777, "none"), (8193, 1024, 777, "swiglu"), (1000, 8192, 1024, "none"), (500, 8192, 500, "relu"),
+    (500, 8192, 512, "none"), (257, 8192, 99, "swiglu"), (6000, 1024, 99, "silu"), (257, 8192, 128, "swiglu"),
+    (20, 8192, 1030, "none"), (20, 2048, 2056, "swiglu"), (20, 1024, 3001, "swiglu"), (6000, 4096, 264, "none"),
+    (20, 1024, 2056, "swiglu"), (20, 512, 3001, "swiglu"), (6000, 8192, 99, "swiglu"), (20, 512, 2056, "swiglu"),
+    (20, 8, 1030, "swiglu"), (3000, 2048, 1, "none"), (2049, 2048, 4096, "swiglu"), (8193, 1024, 1, "gelu"),
+    (3000, 512, 4096, "swiglu"), (257, 2048, 3001, "swiglu"), (20, 8, 2056, "none"), (20, 8192, 500, "swiglu")])
+def test_backward_every_body(M, K, N, act):
+    _backward(M, K, N, act)
 
 
 def test_backward_extreme_preactivations():
