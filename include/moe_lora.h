@@ -540,6 +540,8 @@ int moe_lora_finalize_backward(const moe_lora_shape *shape, const void *d_out, c
  * before any HIP call, concurrent calls with distinct outputs and workspaces);
  * workspaces are 256-byte aligned, their contents on entry do not matter, and
  * their size depends on the shape only.  Results are the same bits in every run.
+ * Every row takes part, a batch's padding too: it adds nothing to the weights'
+ * gradients where its incoming gradients are 0 and its other values finite.
  *
  * Matrix product with an epilogue (the router's logits, a shared expert):
  *   z = x w + bias,  out = act(z) + residual

@@ -713,10 +713,12 @@ def _given(t: Optional[torch.Tensor], dtype, shape, name: str):
 
 
 def _workspace(t: Optional[torch.Tensor]):
-    """(pointer, bytes) of a workspace tensor."""
+    """(pointer, bytes) of a workspace tensor whose device is known."""
     if t is None:
         return None, 0
-    return _ptr(t, None, None, "workspace"), t.numel() * t.element_size()
+    if not t.is_contiguous():
+        _ptr(t, None, None, "workspace")
+    return t.data_ptr(), t.nbytes
 
 
 def _run(index: int, call, *args):
@@ -839,6 +841,9 @@ def block_norm(shape: NormShape, residual: Optional[torch.Tensor], branch: Optio
     return new_residual, normed
 
 
+_NORM_GRADIENTS = ("residual", "branch", "post_weight", "pre_weight", "gate")
+
+
 def block_norm_backward_workspace_size(shape: NormShape) -> int:
     return int(load_library().moe_lora_block_norm_backward_workspace_size(ctypes.byref(shape)))
 
@@ -847,7 +852,7 @@ def block_norm_backward(shape: NormShape, new_residual: Optional[torch.Tensor],
                         branch: Optional[torch.Tensor], post_weight: Optional[torch.Tensor] = None,
                         pre_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
                         d_residual: Optional[torch.Tensor] = None, d_normed: Optional[torch.Tensor] = None,
-                        wanted: Sequence[str] = ("residual", "branch", "post_weight", "pre_weight", "gate"),
+                        wanted: Sequence[str] = _NORM_GRADIENTS,
                         out: Optional[Dict[str, torch.Tensor]] = None,
                         workspace: Optional[torch.Tensor] = None) -> Dict[str, Optional[torch.Tensor]]:
     """Gradients of :func:`block_norm` for those of its outputs, ``d_residual`` and
@@ -864,23 +869,24 @@ def block_norm_backward(shape: NormShape, new_residual: Optional[torch.Tensor],
     gpu = _one_gpu(new_residual, branch, post_weight, pre_weight, gate, d_residual, d_normed, workspace,
                    *out.values())
     token = shape.gate == 1
-    got = dict.fromkeys(("residual", "branch", "post_weight", "pre_weight", "gate"))
+    got = dict.fromkeys(_NORM_GRADIENTS)
     columns = []      # fp32 [H] gradients without a tensor
-    for name, there in (("residual", True), ("branch", branch is not None),
-                        ("post_weight", post_weight is not None),
-                        ("pre_weight", pre_weight is not None and d_normed is not None),
-                        ("gate", gate is not None)):
-        if there and name in wanted:
+    there = (True, branch is not None, post_weight is not None,
+             pre_weight is not None and d_normed is not None, gate is not None)
+    for name, has in zip(_NORM_GRADIENTS, there):
+        if has and name in wanted:
             t = out.get(name)
-            if t is None:
-                if name in ("residual", "branch"):
-                    t = _rows_like(some, rows)
-                elif name == "gate" and token:
-                    t = some.new_empty(shape.rows, dtype=_fp32)
-                else:
-                    columns.append(name)
-            got[name] = t
-    if columns:
+            if t is not None:
+                got[name] = t
+            elif name in ("residual", "branch"):
+                got[name] = _rows_like(some, rows)
+            elif token and name == "gate":
+                got[name] = some.new_empty(shape.rows, dtype=_fp32)
+            else:
+                columns.append(name)
+    if len(columns) == 1:
+        got[columns[0]] = some.new_empty(H, dtype=_fp32)
+    elif columns:
         got.update(zip(columns, some.new_empty((len(columns), H), dtype=_fp32).unbind(0)))
     gate_shape = (shape.rows,) if token else col
     gradients = NormGradients(
