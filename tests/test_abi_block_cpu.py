@@ -281,7 +281,7 @@ def test_matrix_instructions_see_every_lane(tmp_path):
     """MFMA ignores EXEC: none may sit where a branch has narrowed it."""
     from tests.test_isa_mfma_scalar_guards import _mfma_under_exec_mask
     for name in ("linear_tile.hip", "linear_rows.hip"):
-        # the checker reads a kernel to its first end: earlier ones become jumps out of it
+        # the mask check reads a kernel to its first end: earlier ones become jumps out of it
         parts = re.split(r"(?m)^(\.Lfunc_end\d+:)", _asm(name, tmp_path))
         parts = [re.sub(r"s_endpgm(?=[\s\S]*s_endpgm)", "s_branch .LBB_out", part) for part in parts]
         bad, total = _mfma_under_exec_mask("".join(parts))

@@ -83,7 +83,8 @@ def test_forward_large(M, K, N, act):
 @pytest.mark.parametrize("M,K,N,act", [
     (20, 8, 2056, "swiglu"), (8193, 8, 500, "swiglu"), (6000, 8192, 500, "none"), (6000, 8192, 250, "swiglu"),
     (8193, 8, 250, "swiglu"), (4097, 4096, 264, "gelu"), (6000, 4096, 99, "swiglu"), (8193, 8, 250, "silu"),
-    (3000, 8192, 99, "none"), (4097, 4096, 99, "swiglu"), (8193, 8, 8, "swiglu"), (20, 8192, 1, "swiglu")])
+    (3000, 8192, 99, "none"), (4097, 4096, 99, "swiglu"), (8193, 8, 8, "swiglu"), (20, 8192, 1, "swiglu"),
+    (5, 64, 8208, "swiglu")])
 def test_forward_every_body(M, K, N, act):
     _forward(M, K, N, act)
 
