@@ -7,6 +7,7 @@
 #pragma once
 
 #include "device_common.h"
+#include "lds_dma.h"
 
 namespace moe_lora {
 
@@ -31,10 +32,10 @@ __device__ __forceinline__ u32x4 buffer_resource(const char *base)
 // 16 bytes of each lane to lds + 16 lane
 __device__ __forceinline__ void buffer_load_lds16(u32x4 resource, uint32_t offset, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %2\n\t" MOE_LORA_M0_WAIT "buffer_load_dwordx4 %0, %1, 0 offen lds"
                  :
                  : "v"(offset), "s"(resource), "s"(lds)
-                 : "memory");
+                 : "memory", "m0");
 }
 
 // At most N of this wave's loads are still to land and its LDS reads are done; then

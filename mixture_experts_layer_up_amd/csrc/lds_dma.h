@@ -7,7 +7,15 @@
 // the explicit waits below (its own tracking would otherwise wait for every
 // outstanding load before each LDS read and serialise the pipeline).  Loads
 // it does not know about can only make its own wait counts stricter.
+//
+// A load to LDS needs one wait state after the scalar write of M0.  The
+// compiler puts it between the two by itself, but not inside an assembly
+// statement: MOE_LORA_M0_WAIT is that s_nop 0 (0xbf800000), given as its
+// encoding so that the pair "write of M0, load" still stands as two
+// neighbouring lines in the compiler's text, where nothing else may touch M0.
 #pragma once
+
+#define MOE_LORA_M0_WAIT ".long 0xbf800000\n\t"
 
 #include <stdint.h>
 
@@ -24,7 +32,7 @@ __device__ __forceinline__ uint32_t lds_address(const void *p)
 
 __device__ __forceinline__ void load_lds16(const void *g, uint32_t lds_addr)
 {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off"
+    asm volatile("s_mov_b32 m0, %0\n\t" MOE_LORA_M0_WAIT "global_load_lds_dwordx4 %1, off"
                  :
                  : "s"(lds_addr), "v"(g)
                  : "memory", "m0");
@@ -34,7 +42,7 @@ __device__ __forceinline__ void load_lds16(const void *g, uint32_t lds_addr)
 // the stream from evicting data that other blocks are about to reuse.
 __device__ __forceinline__ void load_lds16_stream(const void *g, uint32_t lds_addr)
 {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off nt"
+    asm volatile("s_mov_b32 m0, %0\n\t" MOE_LORA_M0_WAIT "global_load_lds_dwordx4 %1, off nt"
                  :
                  : "s"(lds_addr), "v"(g)
                  : "memory", "m0");
