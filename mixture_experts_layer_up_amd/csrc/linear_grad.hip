@@ -7,11 +7,9 @@
 namespace moe_lora {
 namespace {
 
-// act'(z), not swiglu.  relu: 0 at 0.
+// act'(z) of gelu and silu.
 __device__ __forceinline__ float activation_slope(int act, float z)
 {
-    if (act == MOE_LORA_ACT_RELU)
-        return z > 0.0f ? 1.0f : 0.0f;
     float p, inner;   // of z sigmoid(u(z)): p + z p (1 - p) u'
     if (act == MOE_LORA_ACT_GELU) {
         constexpr float c = 2.0f * 0.79788456080286535588f;
@@ -26,6 +24,16 @@ __device__ __forceinline__ float activation_slope(int act, float z)
     const float q = p * (1.0f - p);
     // past where the sigmoid is 0 or 1 in fp32 the second term is 0 (z inner may be infinite)
     return q == 0.0f ? p : fmaf(z * q, inner, p);
+}
+
+// d act'(z), not swiglu.  relu: 0 where z <= 0, whatever d is (0 times an infinity is not).
+__device__ __forceinline__ float through_activation(int act, float d, float z)
+{
+    if (act == MOE_LORA_ACT_NONE)
+        return d;
+    if (act == MOE_LORA_ACT_RELU)
+        return z > 0.0f ? d : 0.0f;
+    return d * activation_slope(act, z);
 }
 
 constexpr int kTX = 32, kTY = 8;   // threads of a block: 4 columns each, rows
@@ -85,8 +93,8 @@ __global__ __launch_bounds__(kTX *kTY) void act_grad_kernel(ActGradArgs a, int w
                     dup[i] = d[i] * silu_f32(z[i]);
                     d[i] *= up[i] * activation_slope(MOE_LORA_ACT_SILU, z[i]);
                     sum_up[i] += dup[i];
-                } else if (a.act != MOE_LORA_ACT_NONE) {
-                    d[i] *= activation_slope(a.act, z[i]);
+                } else {
+                    d[i] = through_activation(a.act, d[i], z[i]);
                 }
                 sum[i] += d[i];
             }
