@@ -91,7 +91,8 @@ __global__ __launch_bounds__(kTX *kTY) void act_grad_kernel(ActGradArgs a, int w
             for (int i = 0; i < 4; ++i) {
                 if (gated) {
                     dup[i] = d[i] * silu_f32(z[i]);
-                    d[i] *= up[i] * activation_slope(MOE_LORA_ACT_SILU, z[i]);
+                    // the slope first: up slope alone may pass the range where d brings it back
+                    d[i] = d[i] * activation_slope(MOE_LORA_ACT_SILU, z[i]) * up[i];
                     sum_up[i] += dup[i];
                 } else {
                     d[i] = through_activation(a.act, d[i], z[i]);

@@ -1,4 +1,5 @@
-"""Gradients of products whose incoming gradients are infinite or NaN."""
+"""Gradients of products whose incoming gradients are infinite, NaN, or zero beside huge
+pre-activations."""
 import pytest
 import torch
 
@@ -41,3 +42,21 @@ def test_relu_takes_nothing_from_units_that_are_off(M, K, N, fp32):
     assert not torch.isfinite(got["d_x"][m]).any() and torch.equal(got["d_x"][rows], want["d_x"][rows])
     assert not torch.isfinite(got["d_w"][:, n]).any() and torch.equal(got["d_w"][:, cols], want["d_w"][:, cols])
     assert torch.isinf(got["d_bias"][n]) and torch.equal(got["d_bias"][cols], want["d_bias"][cols])
+
+
+@pytest.mark.parametrize("N", [24, 17])
+def test_swiglu_up_values_at_the_end_of_the_range(N):
+    """up slope(gate) alone may pass the range, the gradient with it does not; rows of zero
+    gradients add nothing beside any finite pre-activation."""
+    announce(f"linear_backward swiglu large up {N}")
+    M, K = 40, 64
+    shape, x, w, d, pre = _inputs(M, K, N, "swiglu", 22, False)
+    top = torch.finfo(torch.bfloat16).max
+    pre[:, :N], pre[:, N:] = 2.4, top           # the slope of silu is 1.0998 at 2.4
+    d[::2] = 0
+    d[1::2] = (d[1::2].float() * 1e-35).bfloat16()
+    got = binding.linear_backward(shape, x, w, d, preact=pre, bias_grad=True)
+    want = _block.linear_backward(x, w, d, "swiglu", pre)
+    for name, t in got.items():
+        assert _block.worst(t, *want[name]) <= 1, name
+    assert not got["d_x"][::2].any()
