@@ -587,9 +587,11 @@ int moe_lora_linear(const moe_lora_linear_shape *shape, const void *x, const voi
  *   d_bias = sum over rows of dz, fp32 [W].
  * Each output may be NULL, one at least is given; the residual's gradient is
  * d_out.  relu passes d_out where z > 0 and gives 0 elsewhere, whatever d_out is.
- * dz enters the two products rounded to bf16, d_bias unrounded.  d_x
- * needs w, d_w needs x (else they may be NULL).  With no rows, d_w and d_bias are
- * 0.  d_x may be x itself; outputs overlap nothing else.
+ * dz of a bf16 d_out enters the two products rounded to bf16 once more; of an fp32
+ * d_out it enters with 16 bits, as the sum of two bf16 values, and the products take
+ * up to twice as long.  d_bias takes it unrounded.  d_x needs w, d_w needs x (else
+ * they may be NULL).  With no rows, d_w and d_bias are 0.  d_x may be x itself;
+ * outputs overlap nothing else.
  * x, w, d_out, d_x, d_w and workspace 16-byte (workspace 256-byte) aligned.
  */
 size_t moe_lora_linear_backward_workspace_size(const moe_lora_linear_shape *shape);

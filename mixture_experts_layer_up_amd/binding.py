@@ -781,7 +781,8 @@ def linear_backward(shape: LinearShape, x: Optional[torch.Tensor], w: Optional[t
     """Gradients of :func:`linear` for ``d_out`` [M, N] (typed as its output): ``d_x``
     bf16 [M, K], ``d_w`` bf16 [K, W], ``d_bias`` fp32 [W], None for those not asked
     for.  ``preact`` as the forward wrote it (None without an activation); the
-    residual's gradient is ``d_out`` itself.  ``d_x`` may be ``x``."""
+    residual's gradient is ``d_out`` itself.  ``d_x`` may be ``x``.  A bf16 ``d_out`` is
+    rounded to bf16 again behind the activation; an fp32 one keeps 16 bits there."""
     M, K, N = shape.rows, shape.in_features, shape.out_features
     W = 2 * N if shape.activation == 4 else N
     gpu = _one_gpu(d_out, x, w, preact, d_x, d_w, d_bias, workspace)

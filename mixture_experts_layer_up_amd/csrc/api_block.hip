@@ -112,13 +112,15 @@ struct BackwardLayout {
     bool together;
     int strips;
     bool makes_dz;             // dz is not d_out as it is
+    int parts;                 // bf16 values of one dz
     size_t weight, dz, bias, partial, total;
     explicit BackwardLayout(const Sizes &z, const moe_lora_linear_shape *s)
     {
         const int64_t M = std::max<int64_t>(z.M, 1);
-        dx = plan_product(M, z.K, z.columns(), false);
-        dw = plan_product(z.K, z.columns(), M, false);
-        together = plan_both(M, z.K, z.columns(), &both_dw, &both_dx) <= dx.us + dw.us + 3.0f;
+        parts = s->out_fp32 ? 2 : 1;
+        dx = plan_product(M, z.K, z.columns(), false, parts);
+        dw = plan_product(z.K, z.columns(), M, false, parts);
+        together = plan_both(M, z.K, z.columns(), parts, &both_dw, &both_dx) <= dx.us + dw.us + 3.0f;
         strips = act_grad_blocks(z.M);
         makes_dz = s->activation != MOE_LORA_ACT_NONE || s->out_fp32 || z.padded();
         size_t o = 0;
@@ -128,7 +130,7 @@ struct BackwardLayout {
             return at;
         };
         weight = take(z.padded() ? (size_t)z.K * z.columns() * 2 : 0);
-        dz = take(makes_dz ? (size_t)z.M * z.columns() * 2 : 0);
+        dz = take(makes_dz ? (size_t)z.M * z.columns() * 2 * parts : 0);
         bias = take((size_t)strips * z.width() * sizeof(float));
         // the two products run one after the other
         partial = take(std::max({split_bytes(dx, M, z.K), split_bytes(dw, z.K, z.columns()),
@@ -343,6 +345,7 @@ int moe_lora_linear_backward(const moe_lora_linear_shape *shape, const void *x, 
     char *ws = static_cast<char *>(workspace);
     const bool makes_dz = layout.makes_dz && (d_x || d_w);
     const uint16_t *dz = static_cast<const uint16_t *>(d_out);
+    const int64_t part = layout.parts > 1 ? z.M * z.columns() : 0;
     if (makes_dz || d_bias) {
         ActGradArgs g{};
         g.d_out = d_out;
@@ -351,6 +354,7 @@ int moe_lora_linear_backward(const moe_lora_linear_shape *shape, const void *x, 
         // one strip's sums are the sums
         g.partial = !d_bias ? nullptr : layout.strips == 1 ? d_bias : reinterpret_cast<float *>(ws + layout.bias);
         g.d_bias = d_bias;
+        g.part = part;
         g.M = z.M;
         g.N = z.N;
         g.half = z.half;
@@ -371,6 +375,7 @@ int moe_lora_linear_backward(const moe_lora_linear_shape *shape, const void *x, 
         gw.M = gw.ldq = (int)z.K;
         gw.C = gw.ldp = (int)z.columns();
         gw.K = (int)z.M;
+        gw.part = part;
         gw.partial = partial;
         gw.e.out = d_w;
         gw.e.N = z.padded() ? z.N : (int)z.columns();
@@ -390,6 +395,7 @@ int moe_lora_linear_backward(const moe_lora_linear_shape *shape, const void *x, 
         gx.M = (int)z.M;
         gx.C = (int)z.K;
         gx.K = gx.ldq = gx.ldp = (int)z.columns();
+        gx.part = part;
         gx.partial = partial;
         gx.e.out = d_x;
         gx.e.N = gx.e.half = (int)z.K;

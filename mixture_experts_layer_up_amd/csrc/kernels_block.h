@@ -38,6 +38,7 @@ struct ProductArgs {
     int ldq, ldp;
     int tiles_m, tiles_n;
     int splits, k_per;         // terms a split sums, a multiple of 64
+    int64_t part;              // dz's second part (see ActGradArgs), in elements from the first; 0: none
     float *partial;            // [splits, M, C] when splits > 1
     Epilogue e;
 };
@@ -54,11 +55,12 @@ struct ProductPlan {
     int tiles_m, tiles_n, splits, k_per;
     float us;      // estimate, without a launch's own time
 };
-ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated);
+// `parts` of a gradient: 2 double the steps.
+ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated, int parts = 1);
 hipError_t launch_product(Product kind, const ProductPlan &plan, const ProductArgs &a, hipStream_t s);
 // The weight's and the input's gradient in one launch, with the same tiles, the input's
 // whole: M rows, `in` and `columns` of the weight.  Returns the estimated microseconds.
-float plan_both(int64_t M, int64_t in, int64_t columns, ProductPlan *dw, ProductPlan *dx);
+float plan_both(int64_t M, int64_t in, int64_t columns, int parts, ProductPlan *dw, ProductPlan *dx);
 hipError_t launch_both_gradients(const ProductPlan &dw, const ProductArgs &w, const ProductPlan &dx,
                                  const ProductArgs &x, hipStream_t s);
 
@@ -80,14 +82,15 @@ hipError_t launch_pad_columns(const uint16_t *w, uint16_t *out, int64_t K, int N
                               hipStream_t s);
 
 // dz = d_out act'(preact) as bf16 [M, sets half] (null: not wanted) and partial
-// column sums [blocks, W] (null: not wanted), then d_bias [W] from them.
+// column sums [blocks, W] (null: not wanted), then d_bias [W] from them.  With `part`
+// dz is the sum of two bf16 values, the second `part` elements behind the first.
 struct ActGradArgs {
     const void *d_out;
     const uint16_t *preact;
     uint16_t *dz;
     float *partial;
     float *d_bias;
-    int64_t M;
+    int64_t M, part;
     int N, half, sets, act, fp32;
     int blocks;                // row strips
 };

@@ -36,10 +36,32 @@ __device__ __forceinline__ float through_activation(int act, float d, float z)
     return d * activation_slope(act, z);
 }
 
+__device__ __forceinline__ void store_four(uint16_t *o, const float (&v)[4])
+{
+    *reinterpret_cast<uint2 *>(o) = uint2{float_to_bf16_bits(v[0]) | (float_to_bf16_bits(v[1]) << 16),
+                                          float_to_bf16_bits(v[2]) | (float_to_bf16_bits(v[3]) << 16)};
+}
+
+// What rounding to bf16 leaves of each value (exact); nothing of what has no finite rounding.
+__device__ __forceinline__ void rest_of_four(float (&v)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float first = bf16_bits_to_float(float_to_bf16_bits(v[i]));
+        v[i] = __builtin_fabsf(first) < __builtin_inff() ? v[i] - first : 0.0f;
+    }
+}
+
 constexpr int kTX = 32, kTY = 8;   // threads of a block: 4 columns each, rows
 
 // Block (strip, column group): dz of its rows, and the sums of its columns over them.
 // Bound by memory: d_out and preact in, dz out.
+//
+// dz of a bf16 gradient is rounded to bf16 for the products: one more rounding of what
+// has been rounded so before (with it d_x and d_w are off by 0.0024 of their 2-norm, with
+// their own rounding alone by 0.0017).  An fp32 gradient has no such rounding yet, and keeps
+// 16 bits as the sum of two bf16 values; the products then take twice the steps (8192 rows,
+// 2048 terms, 128 columns with d_bias: 47 us, rounded to one value 34).
 __global__ __launch_bounds__(kTX *kTY) void act_grad_kernel(ActGradArgs a, int wide)
 {
     __shared__ float part[kTY][kTX * 4 * 2];
@@ -101,13 +123,17 @@ __global__ __launch_bounds__(kTX *kTY) void act_grad_kernel(ActGradArgs a, int w
             }
             if (a.dz) {   // columns past N are zeros
                 uint16_t *o = a.dz + m * ((int64_t)a.sets * a.half) + n;
-                *reinterpret_cast<uint2 *>(o) =
-                    uint2{float_to_bf16_bits(d[0]) | (float_to_bf16_bits(d[1]) << 16),
-                          float_to_bf16_bits(d[2]) | (float_to_bf16_bits(d[3]) << 16)};
+                store_four(o, d);
                 if (gated)
-                    *reinterpret_cast<uint2 *>(o + a.half) =
-                        uint2{float_to_bf16_bits(dup[0]) | (float_to_bf16_bits(dup[1]) << 16),
-                              float_to_bf16_bits(dup[2]) | (float_to_bf16_bits(dup[3]) << 16)};
+                    store_four(o + a.half, dup);
+                if (a.part) {
+                    rest_of_four(d);
+                    store_four(o + a.part, d);
+                    if (gated) {
+                        rest_of_four(dup);
+                        store_four(o + a.part + a.half, dup);
+                    }
+                }
             }
         }
     }

@@ -144,7 +144,12 @@ __device__ __forceinline__ void product(const ProductArgs &a, char *lds, int ite
     const int m0 = tm * BM, n0 = tn * (GATED ? BN / 2 : BN);
     const int k0 = split * a.k_per;
     const int K = a.K - k0 < a.k_per ? a.K - k0 : a.k_per;
-    const int steps = (K + BK - 1) / BK;
+    // A gradient in two parts (dz is Q of dz w^T, P of x^T dz): every 64 terms are two steps,
+    // one for each part, and the other operand's are loaded twice, the second time from the
+    // caches.
+    constexpr bool GRADIENT = QS == PS;
+    const int doubled = GRADIENT && a.part != 0;
+    const int steps = ((K + BK - 1) / BK) << doubled;
 
     // rows a tile does not have read as zeros
     Loader<BM, NT, QS> lq;
@@ -166,20 +171,23 @@ __device__ __forceinline__ void product(const ProductArgs &a, char *lds, int ite
     const char *p = reinterpret_cast<const char *>(a.P + (PS ? (size_t)k0 * a.ldp + n0 : (size_t)n0 * a.ldp + k0));
     const size_t q_step = QS ? (size_t)BK * a.ldq * 2 : BK * 2;
     const size_t p_step = PS ? (size_t)BK * a.ldp * 2 : BK * 2;
+    const size_t part = doubled ? (size_t)a.part * 2 : 0;
+    const size_t q_back = QS ? 0 : part, p_back = QS ? part : 0;   // what the first part's step went on
     const uint32_t base = lds_base(lds) + wave * 1024;
 
     // loads of a step past the last read nothing and write zeros: the waits stay the same
     constexpr int kLoads = lq.kLoads + lp.kLoads;
     int next = 0, next_at = 0;
     auto issue = [&](int i) {
-        const int left = K - next * BK;
+        const int left = K - (next >> doubled) * BK;
         if (i < lq.kLoads)
             lq.issue(i, buffer_resource(q), base + next_at, left);
         else
             lp.issue(i - lq.kLoads, buffer_resource(p), base + next_at + kQ, left);
         if (i == kLoads - 1) {
-            q += q_step;
-            p += p_step;
+            const bool first_part = doubled & ~next;
+            q += first_part ? q_back : q_step - q_back;
+            p += first_part ? p_back : p_step - p_back;
             ++next;
             next_at = next_at + kBuffer == kRing ? 0 : next_at + kBuffer;
         }
@@ -480,7 +488,7 @@ void for_splits(int64_t tiles, int64_t K, F f)
 } // namespace
 
 // The tile and split that take the least time by the figures above.
-ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated)
+ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated, int parts)
 {
     ProductPlan best{};
     for (int t = 0; t < kTileShapes; ++t) {
@@ -488,7 +496,7 @@ ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated)
         for_splits(blocks_of(whole), K, [&](int64_t splits) {
             ProductPlan p = cut(t, M, C, K, splits, gated);
             const int64_t each = (blocks_of(cut(t, M, C, K, splits, false)) + kCus - 1) / kCus;   // of the busiest CU
-            const float steps = (float)(p.k_per / BK);
+            const float steps = (float)(p.k_per / BK * parts);
             p.us = steps * (each == 1 ? alone(kTiles[t], blocks_of(p)) : each * kTiles[t].shared) + joining(p, M, C);
             if (best.tiles_m == 0 || p.us < best.us)
                 best = p;
@@ -499,7 +507,7 @@ ProductPlan plan_product(int64_t M, int64_t C, int64_t K, bool gated)
 
 // The same for the two gradients in one launch: the CUs' work in all, the longest block,
 // and what a block takes beside its steps.
-float plan_both(int64_t M, int64_t in, int64_t columns, ProductPlan *dw, ProductPlan *dx)
+float plan_both(int64_t M, int64_t in, int64_t columns, int parts, ProductPlan *dw, ProductPlan *dx)
 {
     float least = 0.0f;
     for (int t = 0; t < kTileShapes; ++t) {
@@ -507,7 +515,7 @@ float plan_both(int64_t M, int64_t in, int64_t columns, ProductPlan *dw, Product
         const ProductPlan x = cut(t, M, in, columns, 1, false), whole = cut(t, in, columns, M, 1, false);
         for_splits(blocks_of(whole), M, [&](int64_t splits) {
             const ProductPlan w = cut(t, in, columns, M, splits, false);
-            const float x_steps = (float)(x.k_per / BK), w_steps = (float)(w.k_per / BK);
+            const float x_steps = (float)(x.k_per / BK * parts), w_steps = (float)(w.k_per / BK * parts);
             const float all = (blocks_of(x) * (x_steps * tile.shared + tile.rest) +
                                blocks_of(w) * (w_steps * tile.shared + tile.rest)) / kCus;
             const float longest = (x_steps > w_steps ? x_steps : w_steps) * alone(tile, blocks_of(x) + blocks_of(w)) +

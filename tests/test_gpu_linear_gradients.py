@@ -1,5 +1,5 @@
-"""Gradients of products whose incoming gradients are infinite, NaN, or zero beside huge
-pre-activations."""
+"""Gradients of products whose incoming gradients are infinite, zero beside huge
+pre-activations, or fp32, against float64."""
 import pytest
 import torch
 
@@ -60,3 +60,52 @@ def test_swiglu_up_values_at_the_end_of_the_range(N):
     for name, t in got.items():
         assert _block.worst(t, *want[name]) <= 1, name
     assert not got["d_x"][::2].any()
+
+
+# fp32 incoming gradients: as many bits of them as two bf16 values hold.  Half a step of the
+# first is at most 2^-8 of the value, of the second at most 2^-8 of the first's error.
+@pytest.mark.parametrize("act", _block.ACTS)
+@pytest.mark.parametrize("M,K,N", [(1, 64, 128), (5, 512, 60), (65, 200, 17), (1000, 512, 128), (333, 416, 99),
+                                   (300, 2048, 2056), (8192, 512, 128), (4100, 264, 130), (2500, 8, 1)])
+def test_fp32_gradients_keep_their_bits(M, K, N, act):
+    announce(f"linear_backward fp32 {M} {K} {N} {act}")
+    shape, x, w, d, pre = _inputs(M, K, N, act, 23, True)
+    got = binding.linear_backward(shape, x, w, d, preact=pre, bias_grad=True)
+    exact = _block.linear_backward(x, w, d, act, pre)
+    again = binding.linear_backward(shape, x.clone(), w, d, preact=pre, bias_grad=True)
+
+    def right(name, t):
+        value, _ = exact[name]
+        assert _block.worst(t, *exact[name]) <= 1, name
+        if t.numel() >= 64 and name != "d_bias":
+            # one rounding of the result, which `once` is, and beside it 2^-16 for dz and
+            # less than as much for fp32 sums and slopes of terms with random signs
+            once = _block.apart(value.bfloat16(), value)
+            assert _block.apart(t, value) <= once + 2.0 ** -14, name
+
+    for name, t in got.items():
+        right(name, t)
+        assert torch.equal(t, again[name]), name
+    # one gradient alone may be summed in other pieces
+    right("d_x", binding.linear_backward(shape, x, w, d, preact=pre, w_grad=False)["d_x"])
+    right("d_w", binding.linear_backward(shape, x, None, d, preact=pre, x_grad=False)["d_w"])
+    inside = x.clone()          # in place: d_w is taken before d_x overwrites x
+    over = binding.linear_backward(shape, inside, w, d, preact=pre, d_x=inside, bias_grad=True)
+    for name, t in over.items():
+        right(name, t)
+
+
+def test_fp32_gradients_that_are_not_finite():
+    """They stay in their rows and columns, and infinities stay infinities."""
+    announce("linear_backward fp32 not finite")
+    for M, K, N in ((40, 72, 17), (700, 264, 128)):
+        shape, x, w, d, _ = _inputs(M, K, N, "none", 24, True)
+        want = binding.linear_backward(shape, x, w, d, bias_grad=True)
+        x[3], w[:, 5] = 1.0, 1.0
+        base = binding.linear_backward(shape, x, w, d, bias_grad=True)
+        d[3, 5] = float("inf")
+        got = binding.linear_backward(shape, x, w, d, bias_grad=True)
+        rows, cols = [i for i in range(M) if i != 3], [i for i in range(N) if i != 5]
+        assert (got["d_x"][3] == float("inf")).all() and (got["d_w"][:, 5] == float("inf")).all()
+        assert torch.equal(got["d_x"][rows], base["d_x"][rows]) and torch.equal(got["d_w"][:, cols], base["d_w"][:, cols])
+        assert float(got["d_bias"][5]) == float("inf") and torch.isfinite(want["d_bias"]).all()
