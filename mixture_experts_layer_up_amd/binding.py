@@ -912,19 +912,18 @@ def _gradients(gradients: Sequence[torch.Tensor], out: Optional[Sequence[torch.T
     """The moe_lora_gradient array of the tensors: four 64-bit words each.  Attribute by
     attribute over all tensors: one by one with their own checks, 60 tensors cost more
     than their kernels."""
-    def row(tensors):
-        return [t.dtype for t in tensors], [t.numel() for t in tensors], [t.data_ptr() for t in tensors]
-
-    kinds, sizes, at = row(gradients)
-    if not {_fp32, _bf16}.issuperset(kinds) or not all([t.is_contiguous() for t in gradients]):
+    pointer, contiguous = torch.Tensor.data_ptr, torch.Tensor.is_contiguous
+    kinds, at = [t.dtype for t in gradients], list(map(pointer, gradients))
+    if not {_fp32, _bf16}.issuperset(kinds) or not all(map(contiguous, gradients)):
         for g in gradients:
             _ptr(g, (_bf16, _fp32), None, "gradient")
-    to = at
+    sizes, to = map(torch.Tensor.numel, gradients), at
     if out is not None:
         if len(out) != len(gradients):
             raise MoELoRAError(f"out has {len(out)} tensors, gradients has {len(gradients)}")
-        out_kinds, out_sizes, to = row(out)
-        if out_kinds != kinds or out_sizes != sizes or not all([t.is_contiguous() for t in out]):
+        to = list(map(pointer, out))
+        if ([t.dtype for t in out] != kinds or [t.shape for t in out] != [t.shape for t in gradients]
+                or not all(map(contiguous, out))):
             for g, o in zip(gradients, out):
                 _ptr(o, g.dtype, g.shape, "out")
     words = array.array("q", itertools.chain.from_iterable(
