@@ -551,7 +551,7 @@ int moe_lora_clip_gradients(const moe_lora_gradient *gradients, int32_t count, f
     hipStream_t st = static_cast<hipStream_t>(stream);
     const int chunk = chunk_of(gradients, count);
     const ClipSums c{reinterpret_cast<double *>(static_cast<char *>(workspace) + kAlign),
-                     total_chunks(gradients, count, chunk), norm, static_cast<float *>(workspace), max_norm};
+                     total_chunks(gradients, count, chunk), norm, static_cast<ClipFactor *>(workspace), max_norm};
     MOE_TRY(for_tables(gradients, count, chunk, [&](const ClipTable &t, int64_t done) {
         return launch_clip_squares(t, c.partial + done, st);
     }));

@@ -110,10 +110,12 @@ __device__ __forceinline__ double chunk_squares(const void *data, int64_t at, in
     return s;
 }
 
+__device__ __forceinline__ float scaled(float v, ClipFactor c) { return v * c.power * c.rest; }
+
 // STREAM is a template argument: of two stores under a branch the compiler makes one,
 // without the hint.
 template <int F32, bool STREAM>
-__device__ __forceinline__ void chunk_scale(const void *data, void *out, int64_t at, int n, float c)
+__device__ __forceinline__ void chunk_scale(const void *data, void *out, int64_t at, int n, ClipFactor c)
 {
     using E = Element<F32>;
     constexpr int kPer = F32 ? 4 : 8;
@@ -121,21 +123,21 @@ __device__ __forceinline__ void chunk_scale(const void *data, void *out, int64_t
     auto *o = static_cast<typename E::type *>(out) + at;
     if ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15) {
         for (int i = threadIdx.x; i < n; i += kThreads)   // 16-byte boundaries differ
-            E::store(o + i, E::load(p + i) * c);
+            E::store(o + i, scaled(E::load(p + i), c));
         return;
     }
     const int head = head_of<F32>(p, n), words = (n - head) / kPer, tail = head + words * kPer;
     if ((int)threadIdx.x < head)
-        E::store(o + threadIdx.x, E::load(p + threadIdx.x) * c);
+        E::store(o + threadIdx.x, scaled(E::load(p + threadIdx.x), c));
     if ((int)threadIdx.x < n - tail)
-        E::store(o + tail + threadIdx.x, E::load(p + tail + threadIdx.x) * c);
+        E::store(o + tail + threadIdx.x, scaled(E::load(p + tail + threadIdx.x), c));
 #pragma unroll 4
     for (int w = threadIdx.x; w < words; w += kThreads) {
         float f[kPer];
         unpack<F32>(load16(p + head + w * kPer), f);
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-            f[i] *= c;
+            f[i] = scaled(f[i], c);
         if constexpr (STREAM)
             store16_stream(o + head + w * kPer, pack<F32>(f));
         else
@@ -173,7 +175,7 @@ __global__ __launch_bounds__(kThreads) void clip_squares_kernel(ClipTable t, dou
 // Sum of all partial sums by THREADS threads, the same bits in every block, and the norm
 // and the factor that come of it.
 template <int THREADS>
-__device__ __forceinline__ float factor_of(const ClipSums &c, float *norm)
+__device__ __forceinline__ ClipFactor factor_of(const ClipSums &c, float *norm)
 {
     __shared__ double part[THREADS / kWave];
     double s = 0.0;
@@ -192,7 +194,12 @@ __device__ __forceinline__ float factor_of(const ClipSums &c, float *norm)
     *norm = (float)total;
     // a norm that is not finite (as the caller sees it): leave the values as they are
     const double f = (double)c.max_norm / (total + 1e-6);
-    return *norm < __builtin_inff() && f < 1.0 ? (float)f : 1.0f;
+    if (!(*norm < __builtin_inff() && f < 1.0))
+        return ClipFactor{1.0f, 1.0f};
+    // below the normal range half of the exponent goes into the power (values of 1e36 scaled
+    // to a norm of 1e-3 would lose the factor's bits)
+    const int e = f > 0.0 && f < 0x1p-126 ? ilogb(f) / 2 : 0;
+    return ClipFactor{(float)ldexp(1.0, e), (float)ldexp(f, -e)};
 }
 
 constexpr int kNormThreads = 1024;
@@ -200,7 +207,7 @@ constexpr int kNormThreads = 1024;
 __global__ __launch_bounds__(kNormThreads) void clip_norm_kernel(ClipSums c)
 {
     float norm;
-    const float f = factor_of<kNormThreads>(c, &norm);
+    const ClipFactor f = factor_of<kNormThreads>(c, &norm);
     if (threadIdx.x == 0) {
         *c.norm = norm;
         *c.factor = f;
@@ -213,7 +220,7 @@ __global__ __launch_bounds__(kNormThreads) void clip_norm_kernel(ClipSums c)
 template <bool FEW, bool STREAM>
 __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable t, ClipSums c, int first_table)
 {
-    float f;
+    ClipFactor f;
     if constexpr (FEW) {
         float norm;
         f = factor_of<kThreads>(c, &norm);
@@ -223,7 +230,7 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable t, ClipS
         f = *c.factor;
     }
     const int i = find_tensor(t, blockIdx.x);
-    if (f == 1.0f && t.t[i].out == t.t[i].data)
+    if (f.power * f.rest == 1.0f && t.t[i].out == t.t[i].data)
         return;
     const int64_t at = (int64_t)((int)blockIdx.x - t.t[i].first) * t.chunk;
     const int64_t left = t.t[i].n - at;

@@ -152,13 +152,19 @@ struct ClipTable {
     bool stream;               // results are written past the caches
 };
 
+// The factor of a call as power * rest; power is 1 where the product is a normal fp32
+// value, else a power of two.  Both 1: leave the values as they are.
+struct ClipFactor {
+    float power, rest;
+};
+
 // What all blocks of a call share: partial[block] = sum of squares of the block's chunk,
 // and what comes of their sum.
 struct ClipSums {
     double *partial;
     int64_t blocks;            // of all launches
     float *norm;
-    float *factor;             // 1: leave the values as they are
+    ClipFactor *factor;
     float max_norm;
 };
 
