@@ -222,15 +222,35 @@ struct Range {
     uintptr_t first, last;
 };
 
-// No range of one tensor meets one of another (a tensor's data and out are its own,
-// and either the same or apart).
-bool ranges_apart(Range *r, int n)
+// Range `which` of a table: the data of tensor which / 2, or its output (odd).
+Range range_of(const moe_lora_gradient *g, int which)
 {
-    auto before = [](const Range &a, const Range &b) { return a.first < b.first; };
-    if (!std::is_sorted(r, r + n, before))
-        std::sort(r, r + n, before);
+    const moe_lora_gradient &t = g[which / 2];
+    const uintptr_t first = reinterpret_cast<uintptr_t>(which & 1 ? t.out : t.data);
+    return Range{first, first + (size_t)t.elements * (t.fp32 ? 4 : 2)};
+}
+
+// No range of one tensor meets one of another (a tensor's data and out are its own,
+// and either the same or apart).  Two bytes of stack a range, and room for no more
+// tensors than a call of that size needs: a caller's thread may have a small stack.
+template <int TENSORS>
+__attribute__((noinline)) bool ranges_apart(const moe_lora_gradient *g, int32_t count, bool scales)
+{
+    static_assert(2 * TENSORS <= 1 << 16, "indices are 16 bits");
+    uint16_t order[2 * TENSORS];
+    int n = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        if (g[i].elements == 0)
+            continue;
+        order[n++] = (uint16_t)(2 * i);
+        if (scales && g[i].out != g[i].data)
+            order[n++] = (uint16_t)(2 * i + 1);
+    }
+    auto before = [g](uint16_t a, uint16_t b) { return range_of(g, a).first < range_of(g, b).first; };
+    if (!std::is_sorted(order, order + n, before))
+        std::sort(order, order + n, before);
     for (int i = 1; i < n; ++i)
-        if (r[i].first < r[i - 1].last)
+        if (range_of(g, order[i]).first < range_of(g, order[i - 1]).last)
             return false;
     return true;
 }
@@ -529,8 +549,6 @@ int moe_lora_clip_gradients(const moe_lora_gradient *gradients, int32_t count, f
     if (!aligned(norm, 4))
         return MOE_LORA_ERR_MISALIGNED;
     const bool scales = !std::isinf(max_norm);
-    Range ranges[2 * kMostTensors];
-    int n = 0;
     for (int32_t i = 0; i < count; ++i) {
         const moe_lora_gradient &g = gradients[i];
         if (g.elements == 0)
@@ -541,11 +559,9 @@ int moe_lora_clip_gradients(const moe_lora_gradient *gradients, int32_t count, f
         const uintptr_t data = reinterpret_cast<uintptr_t>(g.data), out = reinterpret_cast<uintptr_t>(g.out);
         if (data % size != 0 || (scales && out % size != 0))
             return MOE_LORA_ERR_MISALIGNED;
-        ranges[n++] = Range{data, data + (size_t)g.elements * size};
-        if (scales && out != data)
-            ranges[n++] = Range{out, out + (size_t)g.elements * size};
     }
-    if (!ranges_apart(ranges, n))
+    if (!(count <= 128 ? ranges_apart<128>(gradients, count, scales)
+                       : ranges_apart<kMostTensors>(gradients, count, scales)))
         return MOE_LORA_ERR_INVALID_ARG;
     MOE_TRY(check_workspace(workspace, workspace_bytes, moe_lora_clip_workspace_size(gradients, count)));
     hipStream_t st = static_cast<hipStream_t>(stream);
