@@ -263,8 +263,10 @@ hipError_t launch_clip_scale(const ClipTable &t, const ClipSums &c, bool first_t
             hipLaunchKernelGGL((clip_scale_kernel<true, true>), grid, block, 0, s, t, c, first_table);
         else
             hipLaunchKernelGGL((clip_scale_kernel<true, false>), grid, block, 0, s, t, c, first_table);
-    } else {
+    } else if (t.stream) {
         hipLaunchKernelGGL((clip_scale_kernel<false, true>), grid, block, 0, s, t, c, 0);
+    } else {
+        hipLaunchKernelGGL((clip_scale_kernel<false, false>), grid, block, 0, s, t, c, 0);
     }
     return hipGetLastError();
 }

@@ -1,4 +1,5 @@
-"""Clipping with factors below fp32's normal range; outputs of another shape."""
+"""Clipping over more blocks than the scaling blocks sum by themselves, every element
+checked; factors below fp32's normal range; outputs of another shape."""
 import pytest
 import torch
 
@@ -6,10 +7,18 @@ from mixture_experts_layer_up_amd import binding
 from tests import _block
 from tests._gpu import announce
 
+FEW = 4096     # blocks up to which the scaling blocks sum the partial sums
+
+
 def _grads(sizes, seed, scale=1.0, bf16=lambda i: i % 2 == 1):
     g = torch.Generator("cuda").manual_seed(seed)
     flat = torch.randn(sum(sizes), generator=g, device="cuda").split(sizes)
     return [(t * scale).bfloat16() if bf16(i) else t * scale for i, t in enumerate(flat)]
+
+
+def _blocks(grads):
+    """Partial sums of a call, at least (its workspace is rounded up to 32 of them)."""
+    return (binding.clip_workspace_size(grads) - 256) // 8 - 31
 
 
 def _check(grads, max_norm, in_place):
@@ -24,6 +33,48 @@ def _check(grads, max_norm, in_place):
         if pairs:
             t, w = torch.cat([p[0] for p in pairs]), torch.cat([p[1] for p in pairs])
             assert _block.worst(t, w, (half + 4 * _block.U32) * w.abs() + 2.0 ** -133) <= 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("in_place", [False, True])
+def test_many_small_tensors(in_place):
+    """37 tables of a launch each, a few MB in all, tensors of several blocks among them."""
+    announce(f"clip 4096 tensors in_place={in_place}")
+    sizes = [5000 + i if i % 97 == 0 else (37 * i) % 300 + 1 for i in range(4096)]
+    grads = _grads(sizes, 31)
+    assert _blocks(grads) > FEW and sum(sizes) <= 1 << 21
+    _check(grads, 2.0, in_place)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("in_place", [False, True])
+def test_many_tensors_past_the_caches(in_place):
+    """The same with more than 32 MB of results."""
+    announce(f"clip 4096 tensors of 55 MB in_place={in_place}")
+    sizes = [70001 if i % 511 == 0 else (977 * i) % 9000 + 1 for i in range(4096)]
+    grads = _grads(sizes, 32)
+    assert _blocks(grads) > FEW and sum(g.nbytes for g in grads) > 32 << 20
+    _check(grads, 2.0, in_place)
+
+
+@pytest.mark.gpu
+def test_every_value_of_a_large_tensor():
+    n, part = (1 << 31) + 77, 1 << 27
+    announce(f"clip all of {n}")
+    g = torch.Generator("cuda").manual_seed(33)
+    big = torch.empty(n, dtype=torch.bfloat16, device="cuda").normal_(0.0, 0.01, generator=g)
+    small = torch.randn(1000, generator=g, device="cuda")
+    kept, kept_small = big.clone(), small.clone()
+    total = sum(float((big[a:a + part].double() ** 2).sum()) for a in range(0, n, part))
+    total = (total + float((small.double() ** 2).sum())) ** 0.5
+    binding.clip_gradients([big, small], 1.0)
+    f = 1.0 / (total + 1e-6)
+    for a in range(0, n, part):
+        want = kept[a:a + part].double() * f
+        # the factor is off by a rounding of its own and 1e-9 of the norm's sum here
+        assert _block.worst(big[a:a + part], want, (_block.U16 + 4 * _block.U32) * want.abs() + 2.0 ** -133) <= 1, a
+    want = kept_small.double() * f
+    assert _block.worst(small, want, 5 * _block.U32 * want.abs()) <= 1
 
 
 @pytest.mark.gpu
