@@ -87,7 +87,7 @@ struct ForwardLayout {
     size_t weight, partial, total;
     explicit ForwardLayout(const Sizes &z)
     {
-        rows = plan_rows(z.M, z.K, z.N);
+        rows = plan_rows(z.M, z.K, z.N, z.sets);
         plan = ProductPlan{};
         weight = partial = total = 0;
         if (z.M <= 16)

@@ -74,7 +74,7 @@ struct RowsPlan {
     int mt, cpl;   // sixteens of rows a block takes, columns a lane loads; mt 0: too large
     float us;      // estimate
 };
-RowsPlan plan_rows(int64_t M, int64_t K, int64_t N);
+RowsPlan plan_rows(int64_t M, int64_t K, int64_t N, int sets);
 hipError_t launch_rows(const RowsPlan &plan, const RowsArgs &a, hipStream_t s);
 
 // Copy of w [K, sets N] with each projection padded by zeros to `half` columns.

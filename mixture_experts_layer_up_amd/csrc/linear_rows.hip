@@ -172,12 +172,21 @@ hipError_t launch(const RowsArgs &a, hipStream_t s)
 
 // Microseconds of a block on a CU that runs others too: its reduction and epilogue,
 // and its terms.  Fitted to 64 to 1000 rows, 64 to 2048 terms and 128 to 4096 columns
-// within a fifth; a chip with fewer blocks than CUs is up to twice as fast.
+// within a fifth; a chip with fewer blocks than CUs is up to twice as fast.  The second
+// pair: of swiglu, whose blocks have two projections.  It counts where a CU runs several;
+// alone on one such a block takes about as long as the others' among their like (240 shapes of
+// 17 to 1000 rows, 64 to 2048 terms and 8 to 2048 columns, tiles included: 1493 us in all,
+// with the first pair alone 1509, the best of each 1463; 333 rows, 2048 terms, 768 columns
+// 15.2 -> 9.7).
 struct Body {
     int mt, cpl;
     float fixed, term;
+    float fixed_two, term_two;
 };
-constexpr Body kBodies[] = {{1, 1, 0.8f, 0.0017f}, {1, 2, 1.0f, 0.0014f}, {2, 1, 1.2f, 0.0026f}, {2, 2, 1.3f, 0.0019f}};
+constexpr Body kBodies[] = {{1, 1, 0.8f, 0.0017f, 1.4f, 0.0025f},
+                            {1, 2, 1.0f, 0.0014f, 1.7f, 0.0022f},
+                            {2, 1, 1.2f, 0.0026f, 1.3f, 0.0033f},
+                            {2, 2, 1.3f, 0.0019f, 1.75f, 0.0029f}};
 
 template <int SETS>
 hipError_t launch_sets(const RowsPlan &p, const RowsArgs &a, hipStream_t s)
@@ -194,14 +203,16 @@ hipError_t launch_sets(const RowsPlan &p, const RowsArgs &a, hipStream_t s)
 // Up to 16 rows w is read once whatever the width: 4 columns a lane then stream it best
 // (1 row, 4096 x 16384: 21.5 us, two columns 25).  For few blocks one column a lane is
 // best, which gives twice as many (32 rows, 2048 x 60: 4.7, two 7.2).
-RowsPlan plan_rows(int64_t M, int64_t K, int64_t N)
+RowsPlan plan_rows(int64_t M, int64_t K, int64_t N, int sets)
 {
     RowsPlan best{0, 0, 0.0f};
     for (const Body &b : kBodies) {
         if (N % b.cpl != 0 || (b.mt > 1 && M <= 16))
             continue;
         const int64_t blocks = ((N + 16 * b.cpl - 1) / (16 * b.cpl)) * ((M + 16 * b.mt - 1) / (16 * b.mt));
-        const float us = 2.0f + (float)((blocks + 255) / 256) * (b.fixed + b.term * K);
+        const int64_t rounds = (blocks + 255) / 256;
+        const bool two = sets == 2 && rounds > 1;
+        const float us = 2.0f + (float)rounds * (two ? b.fixed_two + b.term_two * K : b.fixed + b.term * K);
         if (blocks < 1 << 20 && (best.mt == 0 || us < best.us))
             best = {b.mt, b.cpl, us};
         if (b.mt == 1 && b.cpl == 1 && blocks <= 128)
