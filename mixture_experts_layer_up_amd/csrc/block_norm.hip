@@ -88,23 +88,29 @@ __global__ __launch_bounds__(TPR > kBlock ? TPR : kBlock) void block_norm_kernel
     for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < a.T; t0 += (int64_t)gridDim.x * kRows) {
         const bool live = t0 + mine < a.T;   // every thread meets the barriers
         const size_t t = live ? t0 + mine : 0, row = t * a.H;
-        float r[NV][8], y[NV][8];
+        int at = lane * 8;
+        if constexpr (NV > 4)   // addresses are found in their turn, not kept for all rows
+            asm("" : "+v"(at));
+        float r[NV][8];
         float sum[1] = {0.0f};
-        u32x4 xv[NV];
+        u32x4 xv[NV], yv[NV];   // as they are until their turn: 64 values a thread fit its registers so
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = (v * TPR + lane) * 8;
+            const int c = v * TPR * 8 + at;
             const bool in = live && c < a.H;
             xv[v] = a.x && in ? load16(a.x + row + c) : zero16();
-            unpack8(a.y && in ? load16(a.y + row + c) : zero16(), y[v]);
+            yv[v] = a.y && in ? load16(a.y + row + c) : zero16();
         }
         float g = a.gate_kind == MOE_LORA_GATE_TOKEN ? static_cast<const float *>(a.gate)[t] : 1.0f;
         if (a.w_post) {
 #pragma unroll
-            for (int v = 0; v < NV; ++v)
+            for (int v = 0; v < NV; ++v) {
+                float y[8];
+                unpack8(yv[v], y);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    sum[0] = fmaf(y[v][i], y[v][i], sum[0]);
+                    sum[0] = fmaf(y[i], y[i], sum[0]);
+            }
             row_sums<TPR>(sum, scratch[turn]);
             turn = turn == 2 ? 0 : turn + 1;
             g *= rsqrtf(sum[0] / a.H + a.eps);
@@ -112,15 +118,18 @@ __global__ __launch_bounds__(TPR > kBlock ? TPR : kBlock) void block_norm_kernel
         sum[0] = 0.0f;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = (v * TPR + lane) * 8;
-            float x[8], w[8], gc[8];
+            const int c = v * TPR * 8 + at;
+            float x[8], y[8], w[8], gc[8];
             unpack8(xv[v], x);
+            if constexpr (NV > 4)   // unpacked again, not kept from the sum of squares
+                asm("" : "+v"(yv[v]));
+            unpack8(yv[v], y);
             unpack8(a.w_post && c < a.H ? load16(a.w_post + c) : zero16(), w);
             unpack8(a.gate_kind == MOE_LORA_GATE_CHANNEL && c < a.H
                         ? load16(static_cast<const uint16_t *>(a.gate) + c) : zero16(), gc);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                float b = g * y[v][i];
+                float b = g * y[i];
                 if (a.w_post)
                     b *= a.offset + w[i];
                 if (a.gate_kind == MOE_LORA_GATE_CHANNEL)
@@ -138,7 +147,7 @@ __global__ __launch_bounds__(TPR > kBlock ? TPR : kBlock) void block_norm_kernel
         const float p = rsqrtf(sum[0] / a.H + a.eps);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = (v * TPR + lane) * 8;
+            const int c = v * TPR * 8 + at;
             if (live && c < a.H) {
                 float w[8];
                 unpack8(load16(a.w_pre + c), w);
@@ -296,11 +305,14 @@ void block_norm_backward_kernel(NormGradArgs a)
             row_values(a, sums, p, mean_q, s, db);
         }
         const float mean_h = a.w_post ? gt * db * inv_h : 0.0f;
+        int at = lane * 8;
+        if constexpr (TPR == 512)   // the outputs' addresses are found here, not kept for all rows
+            asm("" : "+v"(at));
         if (!WIDE && a.d_token && live && lane == 0)
             a.d_token[t] = db;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = first + (v * TPR + lane) * 8;
+            const int c = first + v * TPR * 8 + at;
             float r[8], z[8], y[8], D[8], wq[8], wp[8], g[8], dx[8], dy[8];
             unpack8(now.r[v], r);
             unpack8(now.z[v], z);
