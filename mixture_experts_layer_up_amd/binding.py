@@ -780,8 +780,9 @@ def linear_backward(shape: LinearShape, x: Optional[torch.Tensor], w: Optional[t
                     workspace: Optional[torch.Tensor] = None) -> Dict[str, Optional[torch.Tensor]]:
     """Gradients of :func:`linear` for ``d_out`` [M, N] (typed as its output): ``d_x``
     bf16 [M, K], ``d_w`` bf16 [K, W], ``d_bias`` fp32 [W], None for those not asked
-    for.  ``preact`` as the forward wrote it (None without an activation); the
-    residual's gradient is ``d_out`` itself.  ``d_x`` may be ``x``.  A bf16 ``d_out`` is
+    for (a tensor to write to does not ask: ``d_bias`` needs ``bias_grad``).  ``preact``
+    as the forward wrote it (None without an activation); the residual's gradient is
+    ``d_out`` itself.  ``d_x`` may be ``x``.  A bf16 ``d_out`` is
     rounded to bf16 again behind the activation; an fp32 one keeps 16 bits there."""
     M, K, N = shape.rows, shape.in_features, shape.out_features
     W = 2 * N if shape.activation == 4 else N
@@ -867,6 +868,9 @@ def block_norm_backward(shape: NormShape, new_residual: Optional[torch.Tensor],
     H = shape.hidden
     rows, col = (shape.rows, H), (H,)
     out = out or {}
+    if (out or wanted is not _NORM_GRADIENTS) and not set(_NORM_GRADIENTS).issuperset([*wanted, *out]):
+        raise MoELoRAError(f"gradients are named {', '.join(_NORM_GRADIENTS)}; got "
+                           f"{sorted({*wanted, *out} - {*_NORM_GRADIENTS})}")
     gpu = _one_gpu(new_residual, branch, post_weight, pre_weight, gate, d_residual, d_normed, workspace,
                    *out.values())
     token = shape.gate == 1
