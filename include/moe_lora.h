@@ -644,7 +644,9 @@ int moe_lora_block_norm(const moe_lora_norm_shape *shape, const void *residual, 
  *   d_post_weight, d_pre_weight  fp32 [H] (needs that weight; d_pre_weight needs
  *                           d_normed)
  *   d_gate                  fp32 [T] or [H] as the gate
- * Sums over tokens are fp32 in a fixed order.  d_residual and d_branch may each be
+ * Sums over tokens are fp32 in a fixed order, and so are a row's sums, of products of
+ * new_residual, branch, gate and post_weight too: rows that take them past the fp32
+ * range (values of 1e18) have no finite gradients.  d_residual and d_branch may each be
  * one of the four bf16 [T, H] inputs; outputs overlap nothing else.
  */
 typedef struct moe_lora_norm_gradients {
