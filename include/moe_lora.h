@@ -589,7 +589,8 @@ int moe_lora_linear(const moe_lora_linear_shape *shape, const void *x, const voi
  * d_out.  relu passes d_out where z > 0 and gives 0 elsewhere, whatever d_out is.
  * dz of a bf16 d_out enters the two products rounded to bf16 once more; of an fp32
  * d_out it enters with 16 bits, as the sum of two bf16 values, and the products take
- * up to twice as long.  d_bias takes it unrounded.  d_x needs w, d_w needs x (else
+ * up to twice as long (the shape of a backward call may say fp32 where the forward's
+ * says bf16).  d_bias takes it unrounded.  d_x needs w, d_w needs x (else
  * they may be NULL).  With no rows, d_w and d_bias are 0.  d_x may be x itself;
  * outputs overlap nothing else.
  * x, w, d_out, d_x, d_w and workspace 16-byte (workspace 256-byte) aligned.

@@ -60,8 +60,9 @@ constexpr int kTX = 32, kTY = 8;   // threads of a block: 4 columns each, rows
 // dz of a bf16 gradient is rounded to bf16 for the products: one more rounding of what
 // has been rounded so before (with it d_x and d_w are off by 0.0024 of their 2-norm, with
 // their own rounding alone by 0.0017).  An fp32 gradient has no such rounding yet, and keeps
-// 16 bits as the sum of two bf16 values; the products then take twice the steps (8192 rows,
-// 2048 terms, 128 columns with d_bias: 47 us, rounded to one value 34).
+// 16 bits as the sum of two bf16 values; the products then take twice the steps.  Both ways:
+// 8192 rows, 2048 terms, 128 columns with d_bias 35 and 49 us; 2 x 768 columns, swiglu, 123
+// and 213, too much for bits that a bf16 gradient does not have.
 __global__ __launch_bounds__(kTX *kTY) void act_grad_kernel(ActGradArgs a, int wide)
 {
     __shared__ float part[kTY][kTX * 4 * 2];

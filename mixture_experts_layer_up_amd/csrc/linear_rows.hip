@@ -2,9 +2,11 @@
 // launch:
 //   out[m, n] = epilogue(sum_k x[m, k] w[k, n])
 // Bound by the stream of w (1 row of 4096 x 16384 weights: 21.5 us, 6.2 TB/s) or, below
-// a few MB, by one launch and one chain of loads (1 row of 2048 x 1536: 3.7 us), so w goes from memory straight into MFMA operands: a lane loads CPL
-// neighbouring columns of 8 terms, and one byte permutation per two weights makes
-// K-contiguous fragments of them, without LDS.  The 16 waves of a block split the
+// a few MB, by one launch, one chain of loads and the joining (1 row in graph replays:
+// 2048 x 1536 3.8 us, 2048 x (2 x 768) for swiglu, half as many blocks of twice the weights, 5.0),
+// so w goes from memory straight into MFMA operands: a lane loads CPL neighbouring
+// columns of 8 terms, and one byte permutation per two weights makes K-contiguous
+// fragments of them, without LDS.  The 16 waves of a block split the
 // terms and are joined through LDS in a fixed order.  Any N: CPL divides it.
 #include "device_common.h"
 #include "kernels_block.h"
